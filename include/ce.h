@@ -47,7 +47,8 @@ typedef enum {
     CE_ERR_PATH = 9,     /* a forced path/split cannot run this shape           */
     CE_ERR_SCRATCH = 10, /* ce_fwd_bwd_noalloc: more rows than its static scratch
                             array holds                                          */
-    CE_ERR_REDUCTION = 11 /* reduction is not a ce_reduction                    */
+    CE_ERR_REDUCTION = 11, /* reduction is not a ce_reduction                    */
+    CE_ERR_TEMPERATURE = 12 /* the temperature is not a positive finite number   */
 } ce_status;
 
 /* How the row losses l_b are reduced (ce_fwd_bwd_ex, ce_forward). */
@@ -294,6 +295,70 @@ int ce_release_workspaces(void);
  */
 int ce_fwd_bwd_noalloc(const void *logits, const int32_t *targets, int64_t B, int64_t C,
                        int dtype, float *loss_out, void *grad_out, void *stream);
+
+/*
+ * ce_linear_fwd_bwd -- softmax cross-entropy of a vocabulary projection and
+ * its gradients, without keeping the logits.  For hidden states h[B][D],
+ * weights W[C][D] and targets t[B],
+ *
+ *   z = h W^T,   l_b = logsumexp(z_b) - z_b[t_b],   G = d loss / d z,
+ *   dhidden = G W,   dweight = G^T h,
+ *
+ * with z, the softmax statistics and the loss in fp32.  The logits live one
+ * tile at a time on the chip; when gradients are asked for, their exponentials
+ * are kept in 16 bits for a piece of the rows at a time.
+ *
+ *   hidden, weight  device, row-major contiguous, CE_BF16 or CE_F16 (CE_F32:
+ *                   CE_ERR_DTYPE), 16-byte aligned; D a multiple of 8
+ *                   (CE_ERR_SHAPE).
+ *   targets         device, [B] int32.  A row whose target is `ignore_index`
+ *                   has loss 0 and gradient 0 and does not count for the mean
+ *                   (a mean over no rows is 0, with gradients 0).  Any other
+ *                   target outside [0, C) is a data error as for ce_fwd_bwd.
+ *   ignore_index    any value; one inside [0, C) leaves that class's rows out.
+ *   reduction       a ce_reduction; the mean divides by the rows that count.
+ *   grad_scale      the upstream gradient, as for ce_fwd_bwd_ex.
+ *   loss_out        device: one fp32, or [B] fp32 (CE_REDUCE_NONE).
+ *   dhidden_out     device [B][D] in `dtype`, 16-byte aligned, or NULL.
+ *   dweight_out     device [C][D] in `dtype`, 16-byte aligned, or NULL.  With
+ *                   both NULL the loss alone is computed (scoring, and a
+ *                   server's single tokens).
+ *   stream          a cudaStream_t (NULL = the legacy default stream).
+ *
+ * All memory belongs to the current device (CE_ERR_POINTER).  Outputs are
+ * written, not added to, and may not overlap the inputs or each other.  The
+ * results are the same bits from call to call.  Each probability is rounded to
+ * `dtype` once before the gradients' products (f16: scaled by 2^15, so that
+ * small ones keep their precision); those accumulate in fp32.
+ *
+ * Workspace: the library keeps one per stream, allocated by the first call
+ * that needs it and replaced by a larger one when a call needs more (both may
+ * synchronise): with gradients 2 C bytes for each row of a piece, where a
+ * piece has at most 1 GiB or, with dweight, 4 C D bytes (or 256 rows), and 4 C
+ * D bytes more when dweight is formed from several pieces.  A call captured
+ * into a graph allocates a workspace of its own, which lives until
+ * ce_release_workspaces: such graphs may be replayed on any stream, at the
+ * same time as other calls.  The device error counters are the stream's.
+ */
+int ce_linear_fwd_bwd(const void *hidden, const void *weight, const int32_t *targets, int64_t B,
+                      int64_t D, int64_t C, int dtype, int32_t ignore_index, int reduction,
+                      const float *grad_scale, float *loss_out, void *dhidden_out,
+                      void *dweight_out, void *stream);
+
+/*
+ * ce_linear_distill_fwd_bwd -- ce_distill_fwd_bwd for logits z = h W^T that
+ * are a vocabulary projection, without keeping them: the divergence from a
+ * teacher's top logits, and the gradients of the hidden states and weights.
+ * hidden, weight, dhidden_out, dweight_out, workspace and graphs are as for
+ * ce_linear_fwd_bwd, the teacher's arguments as for ce_distill_fwd_bwd.
+ * The listed classes' logits are formed by fp32 dot products.
+ */
+int ce_linear_distill_fwd_bwd(const void *hidden, const void *weight, const int32_t *teacher_idx,
+                              const void *teacher_val, const float *teacher_lse, int64_t B,
+                              int64_t D, int64_t C, int64_t K, int dtype, int teacher_dtype,
+                              float temperature, int reduction, const float *grad_scale,
+                              float *loss_out, void *dhidden_out, void *dweight_out,
+                              void *stream);
 
 /* Static text for a ce_status value. */
 const char *ce_status_string(int status);

@@ -45,14 +45,15 @@ PATH_NAMES = {CE_PATH_ROWS_WARP: "rows_warp", CE_PATH_ROW_SPLIT: "row_split",
 
 STATUS = {0: "CE_OK", 1: "CE_ERR_NULL", 2: "CE_ERR_SHAPE", 3: "CE_ERR_DTYPE",
           4: "CE_ERR_ALIGN", 5: "CE_ERR_CUDA", 6: "CE_ERR_OVERLAP", 7: "CE_ERR_POINTER",
-          8: "CE_ERR_CAPTURE", 9: "CE_ERR_PATH", 10: "CE_ERR_SCRATCH", 11: "CE_ERR_REDUCTION"}
+          8: "CE_ERR_CAPTURE", 9: "CE_ERR_PATH", 10: "CE_ERR_SCRATCH", 11: "CE_ERR_REDUCTION",
+          12: "CE_ERR_TEMPERATURE"}
 
 # Symbols declared in include/ce.h.
 EXPORTS = ("ce_fwd_bwd", "ce_fwd_bwd_path", "ce_query_plan", "ce_get_device_errors",
            "ce_release_workspaces", "ce_status_string", "ce_last_cuda_error",
            "ce_fwd_bwd_noalloc", "ce_fwd_bwd_ex", "ce_fwd_bwd_ex_path", "ce_forward",
            "ce_softmax_fwd", "ce_softmax_fwd_path", "ce_softmax_bwd", "ce_fwd_bwd_host",
-           "ce_fwd_bwd_host_grad")
+           "ce_fwd_bwd_host_grad", "ce_linear_fwd_bwd", "ce_linear_distill_fwd_bwd")
 # Symbols declared in include/ce_testing.h (test hooks).
 TEST_EXPORTS = ("ce_fwd_bwd_test",)
 
@@ -119,6 +120,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ce_softmax_fwd_path.restype = ci
     lib.ce_softmax_bwd.argtypes = [vp, vp, i64, i64, ci, vp, vp]
     lib.ce_softmax_bwd.restype = ci
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    lib.ce_linear_fwd_bwd.argtypes = [vp, vp, vp, i64, i64, i64, ci, i32, ci, vp, vp, vp, vp, vp]
+    lib.ce_linear_fwd_bwd.restype = ci
+    lib.ce_linear_distill_fwd_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci, f32,
+                                              ci, vp, vp, vp, vp, vp]
+    lib.ce_linear_distill_fwd_bwd.restype = ci
     lib.ce_fwd_bwd_test.argtypes = [vp, vp, i64, i64, ci, vp, vp, vp, ci, ci,
                                     ctypes.POINTER(TestHooks)]
     lib.ce_fwd_bwd_test.restype = ci
@@ -354,6 +361,116 @@ def ce_fwd_bwd_test(logits, targets, loss_out, grad_out, stream=None, path=CE_PA
     _check(lib.ce_fwd_bwd_test(_ptr(logits), _ptr(targets), B, C, _dtype_code(logits),
                                _ptr(loss_out), _ptr(grad_out), _stream_handle(stream), int(path),
                                int(split), ctypes.byref(hooks)))
+
+
+def _check_heads(rows, reduction, loss_out, grad_scale, **others) -> None:
+    """Placement of the tensors of a call (all on the current device, which
+    the C layer's stream belongs to), and the sizes of the loss and the
+    upstream gradient."""
+    import torch
+
+    n = rows if reduction == CE_REDUCE_NONE else 1
+    given = dict(others, loss_out=loss_out, grad_scale=grad_scale)
+    for name, t in given.items():
+        if t is not None and t.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if loss_out is None or loss_out.dtype != torch.float32 or loss_out.numel() < n \
+            or not loss_out.is_contiguous():
+        raise ValueError(f"loss_out must be a contiguous float32 tensor of at least {n} element(s)")
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != n
+                                   or not grad_scale.is_contiguous()):
+        raise ValueError(f"grad_scale must be a contiguous float32 tensor of {n} element(s)")
+    if len({t.device for t in given.values() if t is not None}) != 1:
+        raise ValueError("all tensors must be on one device")
+    if loss_out.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _check_projection(hidden, weight, dhidden_out, dweight_out) -> None:
+    if hidden.dim() != 2 or not hidden.is_contiguous():
+        raise ValueError("hidden must be a contiguous [B, D] tensor")
+    if weight.dim() != 2 or not weight.is_contiguous() or weight.dtype != hidden.dtype \
+            or weight.shape[1] != hidden.shape[1]:
+        raise ValueError("weight must be a contiguous [C, D] tensor of the hidden states' dtype")
+    for name, t, like in (("dhidden_out", dhidden_out, hidden),
+                          ("dweight_out", dweight_out, weight)):
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(like.shape)} "
+                             f"and dtype {like.dtype}")
+
+
+def _check_targets(targets, rows) -> None:
+    import torch
+
+    if (targets is None or targets.dtype != torch.int32 or targets.dim() != 1
+            or targets.numel() != rows or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous [B] int32 tensor")
+
+
+def _check_teacher(teacher_idx, teacher_val, teacher_lse, rows) -> None:
+    import torch
+
+    if teacher_idx.dim() != 2 or teacher_idx.dtype != torch.int32 \
+            or teacher_idx.shape[0] != rows or not teacher_idx.is_contiguous():
+        raise ValueError("teacher_idx must be a contiguous [B, K] int32 tensor")
+    if teacher_val.shape != teacher_idx.shape or not teacher_val.is_contiguous():
+        raise ValueError("teacher_val must be a contiguous [B, K] tensor")
+    if teacher_val.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise TypeError(f"teacher_val must be float32, bfloat16 or float16, got {teacher_val.dtype}")
+    if teacher_lse is not None and (teacher_lse.dtype != torch.float32 or teacher_lse.dim() != 1
+                                    or teacher_lse.numel() != rows
+                                    or not teacher_lse.is_contiguous()):
+        raise ValueError("teacher_lse must be a contiguous [B] float32 tensor")
+
+
+def ce_linear_fwd_bwd(hidden, weight, targets, loss_out, dhidden_out=None, dweight_out=None,
+                      reduction=CE_REDUCE_MEAN, grad_scale=None, ignore_index=-100,
+                      stream=None) -> None:
+    """Softmax cross-entropy of the logits ``hidden @ weight.T`` and its
+    gradients, without keeping the logits.
+
+    hidden       [B, D] bfloat16 or float16 CUDA tensor, D a multiple of 8
+    weight       [C, D] of the same dtype
+    targets      [B] int32; rows whose target is ``ignore_index`` have loss 0
+                 and gradient 0 and are left out of the mean
+    loss_out     float32: one element (mean, sum) or B (none)
+    dhidden_out  like hidden, or None
+    dweight_out  like weight, or None (both None: the loss alone)
+    grad_scale   upstream gradient, one float32 (mean, sum) or [B] (none)
+    """
+    lib = load_library()
+    _check_projection(hidden, weight, dhidden_out, dweight_out)
+    B, D = hidden.shape
+    _check_targets(targets, B)
+    _check_heads(B, reduction, loss_out, grad_scale, hidden=hidden, weight=weight, targets=targets,
+                 dhidden_out=dhidden_out, dweight_out=dweight_out)
+    _check(lib.ce_linear_fwd_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), B, D, weight.shape[0],
+                                 _dtype_code(hidden), int(ignore_index), int(reduction),
+                                 _ptr(grad_scale), _ptr(loss_out), _ptr(dhidden_out),
+                                 _ptr(dweight_out), _stream_handle(stream)))
+
+
+def ce_linear_distill_fwd_bwd(hidden, weight, teacher_idx, teacher_val, loss_out, dhidden_out=None,
+                              dweight_out=None, teacher_lse=None, temperature=1.0,
+                              reduction=CE_REDUCE_MEAN, grad_scale=None, stream=None) -> None:
+    """ce_distill_fwd_bwd of the logits ``hidden @ weight.T`` without keeping
+    them; the projection's tensors as for ce_linear_fwd_bwd, the teacher's as
+    for ce_distill_fwd_bwd."""
+    lib = load_library()
+    _check_projection(hidden, weight, dhidden_out, dweight_out)
+    B, D = hidden.shape
+    _check_teacher(teacher_idx, teacher_val, teacher_lse, B)
+    _check_heads(B, reduction, loss_out, grad_scale, hidden=hidden, weight=weight,
+                 teacher_idx=teacher_idx, teacher_val=teacher_val, teacher_lse=teacher_lse,
+                 dhidden_out=dhidden_out, dweight_out=dweight_out)
+    _check(lib.ce_linear_distill_fwd_bwd(_ptr(hidden), _ptr(weight), _ptr(teacher_idx),
+                                         _ptr(teacher_val), _ptr(teacher_lse), B, D,
+                                         weight.shape[0], teacher_idx.shape[1],
+                                         _dtype_code(hidden), _dtype_code(teacher_val),
+                                         float(temperature), int(reduction), _ptr(grad_scale),
+                                         _ptr(loss_out), _ptr(dhidden_out), _ptr(dweight_out),
+                                         _stream_handle(stream)))
 
 
 def ce_query_plan(B: int, C: int, dtype: int) -> dict:

@@ -16,6 +16,7 @@
 
 #include "../../include/ce.h"
 #include "../../include/ce_testing.h"
+#include "ce_host.h"
 #include "ce_launch.h"
 #include "ce_rows_online.h"
 
@@ -899,6 +900,67 @@ int run_noalloc(const void *logits, const int32_t *targets, int64_t B, int64_t C
 
 namespace ce {
 
+int host_cuda_fail(cudaError_t e) {
+    cudaGetLastError();  // the next launch check is not to see it again
+    return cuda_fail(e);
+}
+
+int host_device(int *dev, int *sms) {
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return host_cuda_fail(e);
+    DeviceInfo d;
+    const int rc = device_info(*dev, &d);
+    if (rc == CE_OK) *sms = d.sms;
+    return rc;
+}
+
+int host_check_device_pointer(const void *p, int dev) {
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();
+        return CE_ERR_POINTER;
+    }
+    if (at.type == cudaMemoryTypeManaged) return CE_OK;
+    return at.type == cudaMemoryTypeDevice && at.device == dev ? CE_OK : CE_ERR_POINTER;
+}
+
+bool host_overlap(const void *a, size_t na, const void *b, size_t nb) {
+    return a && b &&
+           ranges_overlap(reinterpret_cast<uintptr_t>(a), na, reinterpret_cast<uintptr_t>(b), nb);
+}
+
+cudaError_t host_malloc_zeroed(void **p, size_t bytes, size_t zero) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    cudaStream_t s = nullptr;
+    void *q = nullptr;
+    e = cudaMalloc(&q, bytes);
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(q, 0, zero, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (s) cudaStreamDestroy(s);
+    if (e != cudaSuccess && q) cudaFree(q);
+    if (e == cudaSuccess) *p = q;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return e;
+}
+
+int host_error_counters(int dev, cudaStream_t stream, int **err) {
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    Workspace &w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+    if (!w.base) {
+        void *p = nullptr;
+        const size_t bytes = 1 << 16;
+        const cudaError_t e = host_malloc_zeroed(&p, bytes, kHeaderBytes);
+        if (e != cudaSuccess) return host_cuda_fail(e);
+        w.base = static_cast<unsigned char *>(p);
+        w.bytes = bytes;
+    }
+    *err = reinterpret_cast<int *>(w.base + 4);
+    return CE_OK;
+}
+
 cudaError_t ensure_smem_attr(const void *func, int smem) {
     static std::mutex mu;
     static std::map<std::pair<int, const void *>, int> done;
@@ -1317,6 +1379,8 @@ int ce_release_workspaces(void) {
     g_ws.clear();
     g_hs.clear();
     g_ws_retired.clear();
+    const int rc_head = ce::release_head_workspaces();
+    if (rc == CE_OK) rc = rc_head;
     cudaSetDevice(cur);
     return rc;
 }
@@ -1336,6 +1400,7 @@ const char *ce_status_string(int status) {
         case CE_ERR_SCRATCH:
             return "more rows than the static scratch of ce_fwd_bwd_noalloc holds (B <= 262144)";
         case CE_ERR_REDUCTION: return "reduction is not a ce_reduction";
+        case CE_ERR_TEMPERATURE: return "the temperature is not a positive finite number";
         default: return "unknown status";
     }
 }

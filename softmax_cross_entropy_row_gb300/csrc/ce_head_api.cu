@@ -1,0 +1,551 @@
+// C-ABI of the vocabulary projection's operators (ce_linear_fwd_bwd,
+// ce_linear_distill_fwd_bwd in include/ce.h): argument checks, workspaces, the
+// tensor maps of the operands and the sequence of launches.  Nothing here
+// computes on the host.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <tuple>
+#include <vector>
+
+#include "../../include/ce.h"
+#include "ce_head_gemm.h"
+#include "ce_head_rows.h"
+#include "ce_host.h"
+
+namespace {
+
+// ------------------------------------------------------------- workspaces
+//
+// One per (device, stream), grown when a call needs more; nothing but the
+// calls of that stream uses it, so an outgrown one is freed once the stream
+// has drained.  A call that is being captured into a graph gets a workspace
+// that belongs to that capture alone, so graphs may be replayed at the same
+// time as each other and as eager calls; it is kept until
+// ce_release_workspaces.
+struct Buffer {
+    unsigned char *base = nullptr;
+    size_t bytes = 0;
+};
+std::mutex g_mu;  // held over a whole call: its launches use the workspace
+std::map<std::tuple<int, uintptr_t, unsigned long long>, Buffer> g_buffers;
+std::vector<std::pair<int, unsigned char *>> g_outgrown;  // of captures
+
+int workspace(int dev, cudaStream_t s, size_t need, unsigned char **out) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamGetCaptureInfo(s, &cs, &id);
+    if (e != cudaSuccess) return ce::host_cuda_fail(e);
+    if (cs != cudaStreamCaptureStatusActive) id = 0;
+    Buffer &b = g_buffers[{dev, reinterpret_cast<uintptr_t>(s), id}];
+    if (b.bytes < need) {
+        if (b.base) {
+            if (id) {
+                g_outgrown.push_back({dev, b.base});
+            } else {
+                e = cudaStreamSynchronize(s);
+                if (e == cudaSuccess) e = cudaFree(b.base);
+                if (e != cudaSuccess) return ce::host_cuda_fail(e);
+            }
+            b = Buffer();
+        }
+        const size_t bytes = (need + (1 << 20) - 1) >> 20 << 20;
+        void *p = nullptr;
+        e = ce::host_malloc_zeroed(&p, bytes, 256);
+        if (e != cudaSuccess) return ce::host_cuda_fail(e);
+        b.base = static_cast<unsigned char *>(p);
+        b.bytes = bytes;
+    }
+    *out = b.base;
+    return CE_OK;
+}
+
+// ------------------------------------------------------------ tensor maps
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encode_function(EncodeTiled *out) {
+    static std::mutex mu;
+    static EncodeTiled fn = nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!fn) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                               cudaEnableDefault, &found);
+        if (e != cudaSuccess) return ce::host_cuda_fail(e);
+        if (found != cudaDriverEntryPointSuccess || !f)
+            return ce::host_cuda_fail(cudaErrorNotSupported);
+        fn = reinterpret_cast<EncodeTiled>(f);
+    }
+    *out = fn;
+    return CE_OK;
+}
+
+// [rows][cols] with `ld` elements from row to row; boxes of box_rows x (128
+// bytes), 128-byte swizzled in shared memory.
+int tensor_map(CUtensorMap *map, int dtype, const void *base, long long rows, long long cols,
+               long long ld, int box_rows) {
+    EncodeTiled encode;
+    const int rc = encode_function(&encode);
+    if (rc != CE_OK) return rc;
+    const int es = dtype == CE_F32 ? 4 : 2;
+    const CUtensorMapDataType type = dtype == CE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == CE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = encode(map, type, 2, const_cast<void *>(base), dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? CE_OK : ce::host_cuda_fail(cudaErrorInvalidValue);
+}
+
+// ------------------------------------------------------------------ plans
+
+constexpr long long kMaxK = 1024;             // places of a teacher's list
+constexpr long long kPieceBytes = 1LL << 30;  // kept exponentials, see rows_per_piece
+
+long long round_up(long long v, long long a) { return (v + a - 1) / a * a; }
+long long ceil_div(long long v, long long a) { return (v + a - 1) / a; }
+
+// Rows whose exponentials are kept at a time.  Several pieces need the
+// weights' gradient accumulated in fp32 (4 C D bytes), so a piece is allowed
+// as much as that buffer would take: a batch that fits needs no buffer.
+long long rows_per_piece(long long B, long long D, long long C, bool dweight) {
+    long long bytes = kPieceBytes;
+    if (dweight) bytes = std::max(bytes, 4 * C * D);
+    const long long r = bytes / (2 * round_up(C, 64)) / ce::kTileM * ce::kTileM;
+    return std::min(round_up(B, ce::kTileM), std::max<long long>(r, ce::kTileM));
+}
+
+// Parts of a contraction of kb stages over `tiles` tiles: the number that
+// gives the least time by count of waves, a stage of a tile taking 0.3 us and
+// an fp32 part of a tile 2 x 256 KB at the memory's rate over all SMs.
+int parts_of(long long tiles, long long kb, int pairs) {
+    double best = 1e30;
+    int splits = 1;
+    for (int s = 1; s <= 32 && s <= std::max<long long>(1, kb / 4); ++s) {
+        const double waves = (double)ceil_div(tiles * s, pairs);
+        const double t = waves * (double)ceil_div(kb, s) * 0.3 +
+                         (s > 1 ? 4.0 + (double)tiles * s * 2.0 * 0.262144 / 6.7 : 0.0);
+        if (t < best * 0.97) {
+            best = t;
+            splits = s;
+        }
+    }
+    return splits;
+}
+
+struct Call {
+    const void *hidden, *weight;
+    const int32_t *targets;  // cross-entropy
+    int ignore_index;
+    const int32_t *idx;  // teacher
+    const void *val;
+    const float *lse;
+    int64_t K;
+    int teacher_dtype;
+    float temperature;
+    int64_t B, D, C;
+    int dtype, reduction;
+    const float *scale;
+    float *loss;
+    void *dhidden, *dweight;
+    void *stream;
+};
+
+int check(const Call &c) {
+    const bool teacher = c.targets == nullptr;
+    if (c.dtype != CE_BF16 && c.dtype != CE_F16) return CE_ERR_DTYPE;
+    if (teacher && c.teacher_dtype != CE_F32 && c.teacher_dtype != CE_BF16 &&
+        c.teacher_dtype != CE_F16)
+        return CE_ERR_DTYPE;
+    if (c.reduction != CE_REDUCE_MEAN && c.reduction != CE_REDUCE_SUM &&
+        c.reduction != CE_REDUCE_NONE)
+        return CE_ERR_REDUCTION;
+    if (!c.hidden || !c.weight || !c.loss) return CE_ERR_NULL;
+    if (teacher && (!c.idx || !c.val)) return CE_ERR_NULL;
+    if (c.B < 1 || c.C < 1 || c.D < 8 || c.D % 8 || c.B > 0x7fffff00LL || c.C > 0x7fffff00LL ||
+        c.D > (1 << 24))
+        return CE_ERR_SHAPE;
+    if (teacher && (c.K < 1 || c.K > kMaxK)) return CE_ERR_SHAPE;
+    if (ceil_div(c.C, ce::kTileN) * ceil_div(std::max(c.B, c.D), ce::kTileM) * 32 > 0x7fffffffLL ||
+        ceil_div(c.B, ce::kTileM) * ceil_div(c.D, ce::kTileM) * 32 > 0x7fffffffLL)
+        return CE_ERR_SHAPE;
+    if (teacher && !(c.temperature > 0.f && isfinite(c.temperature))) return CE_ERR_TEMPERATURE;
+    const auto off = [](const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a; };
+    const uintptr_t te = c.teacher_dtype == CE_F32 ? 4 : 2;
+    if (off(c.hidden, 16) || off(c.weight, 16) || off(c.dhidden, 16) || off(c.dweight, 16) ||
+        off(c.targets, 4) || off(c.idx, 4) || off(c.val, te) || off(c.lse, 4) || off(c.scale, 4) ||
+        off(c.loss, 4))
+        return CE_ERR_ALIGN;
+    const size_t rows = c.reduction == CE_REDUCE_NONE ? (size_t)c.B * 4 : 4;
+    const size_t hb = (size_t)c.B * c.D * 2, wb = (size_t)c.C * c.D * 2;
+    struct Range {
+        const void *p;
+        size_t n;
+    };
+    const Range in[] = {{c.hidden, hb},
+                        {c.weight, wb},
+                        {c.targets, (size_t)c.B * 4},
+                        {c.idx, (size_t)c.B * c.K * 4},
+                        {c.val, (size_t)c.B * c.K * te},
+                        {c.lse, (size_t)c.B * 4},
+                        {c.scale, rows}};
+    const Range out[] = {{c.loss, rows}, {c.dhidden, hb}, {c.dweight, wb}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range &r : in)
+            if (ce::host_overlap(out[i].p, out[i].n, r.p, r.n)) return CE_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (ce::host_overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return CE_ERR_OVERLAP;
+    }
+    return CE_OK;
+}
+
+// Hands out the workspace's parts, 256-byte aligned (first pass: sizes alone).
+struct Carver {
+    unsigned char *base = nullptr;
+    size_t used = 256;  // HeadInfo
+    template <typename T>
+    T *take(size_t n) {
+        T *p = reinterpret_cast<T *>(base + used);
+        used += (n * sizeof(T) + 255) / 256 * 256;
+        return p;
+    }
+};
+
+struct Parts {
+    ce::HeadInfo *info;
+    float *loss, *zt, *logq, *zk, *mass, *hidden_parts, *weight_parts;
+    float2 *stats;
+    ce::HeadRow *row;
+    unsigned char *exps;
+};
+
+struct Sizes {
+    long long piece, pieces, ld, tiles;       // rows per piece, pieces, exponentials' row, tiles
+    int hidden_splits, weight_splits;
+    long long hidden_slab, weight_slab;       // rows of an fp32 part
+    bool weight_f32;
+};
+
+Parts carve(Carver &w, const Call &c, const Sizes &z) {
+    const bool teacher = c.targets == nullptr, grad = c.dhidden || c.dweight;
+    Parts p = {};
+    p.info = reinterpret_cast<ce::HeadInfo *>(w.base);
+    p.loss = w.take<float>(c.reduction == CE_REDUCE_NONE ? 0 : round_up(c.B, 1024));
+    p.stats = w.take<float2>((size_t)z.tiles * z.piece);
+    p.row = w.take<ce::HeadRow>(z.piece);
+    p.zt = w.take<float>(teacher ? 0 : z.piece);
+    p.logq = w.take<float>(teacher ? (size_t)c.B * c.K : 0);
+    p.zk = w.take<float>(teacher ? (size_t)c.B * c.K : 0);
+    p.mass = w.take<float>(teacher ? c.B : 0);
+    p.exps = w.take<unsigned char>(grad ? (size_t)z.piece * z.ld * 2 : 0);
+    p.hidden_parts = w.take<float>(c.dhidden && z.hidden_splits > 1
+                                       ? (size_t)z.hidden_splits * z.hidden_slab * c.D : 0);
+    p.weight_parts = w.take<float>(c.dweight && z.weight_f32
+                                       ? (size_t)z.weight_splits * z.weight_slab * c.D : 0);
+    return p;
+}
+
+#define CE_TRY(x)                                    \
+    do {                                             \
+        const int rc_ = (x);                         \
+        if (rc_ != CE_OK) return rc_;                \
+    } while (0)
+#define CE_CUDA(x)                                             \
+    do {                                                       \
+        const cudaError_t e_ = (x);                            \
+        if (e_ != cudaSuccess) return ce::host_cuda_fail(e_);  \
+    } while (0)
+
+int run(const Call &c) {
+    CE_TRY(check(c));
+    int dev = 0, sms = 0;
+    CE_TRY(ce::host_device(&dev, &sms));
+    for (const void *p : {c.hidden, c.weight, (const void *)c.targets, (const void *)c.idx, c.val,
+                          (const void *)c.lse, (const void *)c.scale, (const void *)c.loss,
+                          (const void *)c.dhidden, (const void *)c.dweight})
+        if (p) CE_TRY(ce::host_check_device_pointer(p, dev));
+    cudaStream_t s = static_cast<cudaStream_t>(c.stream);
+    int *err = nullptr;
+    CE_TRY(ce::host_error_counters(dev, s, &err));
+
+    const bool teacher = c.targets == nullptr, grad = c.dhidden || c.dweight;
+    const bool bf16 = c.dtype == CE_BF16, none = c.reduction == CE_REDUCE_NONE;
+    const int pairs = sms / 2;
+    Sizes z = {};
+    z.ld = round_up(c.C, 64);
+    z.tiles = ceil_div(c.C, ce::kTileN);
+    z.piece = grad ? rows_per_piece(c.B, c.D, c.C, c.dweight != nullptr)
+                   : std::min(round_up(c.B, ce::kTileM),
+                              std::max<long long>(ce::kTileM, kPieceBytes / (8 * z.tiles) /
+                                                                  ce::kTileM * ce::kTileM));
+    z.pieces = ceil_div(c.B, z.piece);
+    z.piece = std::min<long long>(z.piece, c.B);
+    z.hidden_slab = round_up(z.piece, ce::kTileM);
+    z.weight_slab = round_up(c.C, ce::kTileM);
+    z.hidden_splits = parts_of(ceil_div(z.piece, ce::kTileM) * ceil_div(c.D, ce::kTileN),
+                               ceil_div(c.C, ce::kTileK), pairs);
+    z.weight_splits = parts_of(z.tiles * ceil_div(c.D, ce::kTileN),
+                               ceil_div(z.piece, ce::kTileK), pairs);
+    z.weight_f32 = z.pieces > 1 || z.weight_splits > 1;
+    if (z.hidden_slab * z.hidden_splits > 0x7fffffffLL ||
+        z.weight_slab * z.weight_splits > 0x7fffffffLL)
+        return CE_ERR_SHAPE;
+
+    std::lock_guard<std::mutex> lk(g_mu);
+    Carver sizer;
+    carve(sizer, c, z);
+    Carver w;
+    CE_TRY(workspace(dev, s, sizer.used, &w.base));
+    const Parts ws = carve(w, c, z);
+
+    // f16 holds values down to 2^-24: the kept values (at most 1) are raised
+    // by 2^15 so that small probabilities keep their 11 bits
+    const float shift = bf16 ? 0.f : 15.f;
+    const float shift_mul = bf16 ? 1.f : 32768.f;
+    const float *row_scale = none ? c.scale : nullptr;
+
+    ce::HeadTeacher t = {};
+    if (teacher) {
+        t.B = c.B;
+        t.D = (int)c.D;
+        t.C = (int)c.C;
+        t.K = (int)c.K;
+        t.hidden = static_cast<const unsigned char *>(c.hidden);
+        t.weight = static_cast<const unsigned char *>(c.weight);
+        t.idx = c.idx;
+        t.val = c.val;
+        t.val_dtype = c.teacher_dtype;
+        t.lse = c.lse;
+        t.inv_t = 1.f / c.temperature;
+        t.logq = ws.logq;
+        t.zk = ws.zk;
+        t.mass = ws.mass;
+        t.err = err;
+        CE_CUDA(ce::launch_head_teacher(t, bf16, sms, s));
+    }
+    if (grad || c.reduction == CE_REDUCE_MEAN) {
+        ce::HeadPrep p = {};
+        p.B = c.B;
+        p.targets = c.targets;
+        p.ignore_index = c.ignore_index;
+        p.mass = teacher ? ws.mass : nullptr;
+        p.scale = c.scale;
+        p.scale_per_row = row_scale != nullptr;
+        p.mean = c.reduction == CE_REDUCE_MEAN;
+        p.alpha = (teacher ? c.temperature : 1.f) / shift_mul;
+        p.info = ws.info;
+        CE_CUDA(ce::launch_head_prep(p, s));
+    }
+
+    float *loss_rows = none ? c.loss : ws.loss;
+    for (long long i = 0; i < z.pieces; ++i) {
+        const long long b0 = i * z.piece;
+        const long long rows = std::min<long long>(z.piece, c.B - b0);
+        const unsigned char *h =
+            static_cast<const unsigned char *>(c.hidden) + (size_t)b0 * c.D * 2;
+        ce::HeadGemm g = {};
+        CE_TRY(tensor_map(&g.a, c.dtype, h, rows, c.D, c.D, ce::kTileM / 2));
+        CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileN / 2));
+        if (grad) CE_TRY(tensor_map(&g.out, c.dtype, ws.exps, rows, z.ld, z.ld, 32));
+        g.tiles_m = (int)ceil_div(rows, ce::kTileM);
+        g.tiles_n = (int)z.tiles;
+        g.splits = 1;
+        g.k_blocks = (int)ceil_div(c.D, ce::kTileK);
+        g.group_m = std::min(g.tiles_m, 16);
+        g.exp_scale = ce::kLog2e / (teacher ? c.temperature : 1.f);
+        g.shift = shift;
+        g.rows = (int)rows;
+        g.cols = (int)c.C;
+        g.targets = teacher ? nullptr : c.targets + b0;
+        g.stats = ws.stats;
+        g.zt = ws.zt;
+        g.write_exp = grad ? 1 : 0;
+        g.failed = &ws.info->failed;
+        g.clear_failed = i == 0;
+        g.err = err;
+        CE_CUDA(ce::launch_head_gemm(g, ce::kProdLogits, ce::kEpiLogits, bf16, sms, s));
+
+        ce::HeadRows r = {};
+        r.rows = (int)rows;
+        r.cols = (int)c.C;
+        r.tiles = (int)z.tiles;
+        r.stats = ws.stats;
+        r.zt = ws.zt;
+        r.row = ws.row;
+        r.exps = ws.exps;
+        r.ld = z.ld;
+        r.exp_scale = g.exp_scale;
+        r.temperature = c.temperature;
+        r.shift_mul = shift_mul;
+        r.targets = g.targets;
+        r.ignore_index = c.ignore_index;
+        if (teacher) {
+            r.logq = ws.logq + b0 * c.K;
+            r.idx = c.idx + b0 * c.K;
+            r.zk = ws.zk + b0 * c.K;
+            r.mass = ws.mass + b0;
+            r.K = (int)c.K;
+        }
+        r.row_scale = row_scale ? row_scale + b0 : nullptr;
+        r.info = ws.info;
+        r.err = err;
+        r.loss = loss_rows + b0;
+        r.want_grad = grad;
+        r.nan_on_failure = none && !grad;
+        CE_CUDA(ce::launch_head_rows(r, s));
+        if (grad) CE_CUDA(ce::launch_head_scale(r, bf16, s));
+        if (teacher) CE_CUDA(ce::launch_head_listed(r, bf16, s));
+
+        g.clear_failed = 0;
+        g.cols = (int)c.D;
+        g.scale = &ws.info->out;
+        g.alpha = 1.f;
+        if (c.dhidden) {
+            unsigned char *dh = static_cast<unsigned char *>(c.dhidden) + (size_t)b0 * c.D * 2;
+            const bool split = z.hidden_splits > 1;
+            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, rows, z.ld, z.ld, ce::kTileM / 2));
+            CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileK));
+            if (split)
+                CE_TRY(tensor_map(&g.out, CE_F32, ws.hidden_parts,
+                                  z.hidden_slab * z.hidden_splits, c.D, c.D, 32));
+            else
+                CE_TRY(tensor_map(&g.out, c.dtype, dh, rows, c.D, c.D, 32));
+            g.tiles_m = (int)ceil_div(rows, ce::kTileM);
+            g.tiles_n = (int)ceil_div(c.D, ce::kTileN);
+            g.splits = z.hidden_splits;
+            g.k_blocks = (int)ceil_div(c.C, ce::kTileK);
+            g.group_m = std::min(g.tiles_m, 8);
+            g.split_rows = z.hidden_slab;
+            g.rows = (int)rows;
+            CE_CUDA(ce::launch_head_gemm(g, ce::kProdHidden, split ? ce::kEpiF32 : ce::kEpiOut,
+                                         bf16, sms, s));
+            if (split)
+                CE_CUDA(ce::launch_head_join(ws.hidden_parts, rows * c.D, z.hidden_slab * c.D,
+                                             z.hidden_splits, &ws.info->out, 1.f, dh, bf16, sms,
+                                             s));
+        }
+        if (c.dweight) {
+            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, rows, z.ld, z.ld, ce::kTileK));
+            CE_TRY(tensor_map(&g.b, c.dtype, h, rows, c.D, c.D, ce::kTileK));
+            if (z.weight_f32)
+                CE_TRY(tensor_map(&g.out, CE_F32, ws.weight_parts,
+                                  z.weight_slab * z.weight_splits, c.D, c.D, 32));
+            else
+                CE_TRY(tensor_map(&g.out, c.dtype, c.dweight, c.C, c.D, c.D, 32));
+            g.tiles_m = (int)z.tiles;
+            g.tiles_n = (int)ceil_div(c.D, ce::kTileN);
+            g.k_blocks = (int)ceil_div(rows, ce::kTileK);
+            g.splits = z.weight_splits;
+            g.group_m = std::min(g.tiles_m, 8);
+            g.split_rows = z.weight_slab;
+            g.rows = (int)c.C;
+            CE_CUDA(ce::launch_head_gemm(g, ce::kProdWeight,
+                                         !z.weight_f32 ? ce::kEpiOut
+                                         : i == 0      ? ce::kEpiF32
+                                                       : ce::kEpiAdd,
+                                         bf16, sms, s));
+        }
+    }
+    if (c.dweight && z.weight_f32)
+        CE_CUDA(ce::launch_head_join(ws.weight_parts, c.C * c.D, z.weight_slab * c.D,
+                                     z.weight_splits, &ws.info->out, 1.f, c.dweight, bf16, sms, s));
+    if (!none || grad)
+        CE_CUDA(ce::launch_head_loss(loss_rows, c.B, c.reduction, ws.info, c.loss, s));
+    return CE_OK;
+}
+
+}  // namespace
+
+namespace ce {
+
+int release_head_workspaces() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int rc = CE_OK;
+    for (auto &kv : g_buffers) {
+        if (!kv.second.base) continue;
+        cudaSetDevice(std::get<0>(kv.first));
+        const cudaError_t e = cudaFree(kv.second.base);
+        if (e != cudaSuccess) rc = host_cuda_fail(e);
+    }
+    for (auto &b : g_outgrown) {
+        cudaSetDevice(b.first);
+        const cudaError_t e = cudaFree(b.second);
+        if (e != cudaSuccess) rc = host_cuda_fail(e);
+    }
+    g_buffers.clear();
+    g_outgrown.clear();
+    return rc;
+}
+
+}  // namespace ce
+
+extern "C" {
+
+int ce_linear_fwd_bwd(const void *hidden, const void *weight, const int32_t *targets, int64_t B,
+                      int64_t D, int64_t C, int dtype, int32_t ignore_index, int reduction,
+                      const float *grad_scale, float *loss_out, void *dhidden_out,
+                      void *dweight_out, void *stream) {
+    if (!targets) return CE_ERR_NULL;
+    Call c = {};
+    c.hidden = hidden;
+    c.weight = weight;
+    c.targets = targets;
+    c.ignore_index = ignore_index;
+    c.temperature = 1.f;
+    c.B = B;
+    c.D = D;
+    c.C = C;
+    c.dtype = dtype;
+    c.reduction = reduction;
+    c.scale = grad_scale;
+    c.loss = loss_out;
+    c.dhidden = dhidden_out;
+    c.dweight = dweight_out;
+    c.stream = stream;
+    return run(c);
+}
+
+int ce_linear_distill_fwd_bwd(const void *hidden, const void *weight, const int32_t *teacher_idx,
+                              const void *teacher_val, const float *teacher_lse, int64_t B,
+                              int64_t D, int64_t C, int64_t K, int dtype, int teacher_dtype,
+                              float temperature, int reduction, const float *grad_scale,
+                              float *loss_out, void *dhidden_out, void *dweight_out,
+                              void *stream) {
+    Call c = {};
+    c.hidden = hidden;
+    c.weight = weight;
+    c.idx = teacher_idx;
+    c.val = teacher_val;
+    c.lse = teacher_lse;
+    c.K = K;
+    c.teacher_dtype = teacher_dtype;
+    c.temperature = temperature;
+    c.B = B;
+    c.D = D;
+    c.C = C;
+    c.dtype = dtype;
+    c.reduction = reduction;
+    c.scale = grad_scale;
+    c.loss = loss_out;
+    c.dhidden = dhidden_out;
+    c.dweight = dweight_out;
+    c.stream = stream;
+    return run(c);
+}
+
+}  // extern "C"
