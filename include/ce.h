@@ -346,6 +346,47 @@ int ce_linear_fwd_bwd(const void *hidden, const void *weight, const int32_t *tar
                       void *dweight_out, void *stream);
 
 /*
+ * ce_distill_fwd_bwd -- distillation from a teacher's top logits: the
+ * divergence of each row's softmax from the teacher's probabilities over a
+ * list of K classes, and its gradient.  With temperature T, p = softmax(z_b /
+ * T) over all classes, and the list (i_k, t_k),
+ *
+ *   q_k = softmax(t / T)_k over the row's list (teacher_lse NULL), or
+ *   q_k = exp(t_k / T - teacher_lse[b])        (the teacher's own normaliser,
+ *                                               logsumexp(t / T) over all of
+ *                                               its classes),
+ *   l_b = T^2 sum_k q_k (log q_k - log p_{i_k}),
+ *   grad[b][c] = f_b T (Q_b p_c - sum_{k: i_k = c} q_k),   Q_b = sum_k q_k,
+ *
+ * f_b = 1/B (mean) or 1, times the upstream gradient.
+ *
+ *   logits       device, [B][C] row-major contiguous, any ce_dtype.
+ *   teacher_idx  device, [B][K] int32 classes.  -1: the place is unused
+ *                (whatever teacher_val holds there).  A row without a used
+ *                place has loss 0 and gradient 0 (it counts for the mean).  A
+ *                class may be listed more than once: its places add up.  A
+ *                class below -1 or not below C is a data error: the row's loss
+ *                is NaN, its gradient leaves that place out, and the stream's
+ *                bad-target count rises by one for the row.
+ *   teacher_val  device, [B][K] of `teacher_dtype` (any ce_dtype).  -inf:
+ *                probability 0.
+ *   teacher_lse  device [B] fp32, or NULL.
+ *   K            1 .. 1024 (CE_ERR_SHAPE).
+ *   temperature  positive and finite (CE_ERR_TEMPERATURE).
+ *   reduction, grad_scale, loss_out: as for ce_fwd_bwd_ex.
+ *   grad_out     device [B][C] in `dtype`, or NULL: the loss alone.
+ *
+ * Pointers are aligned to their element size and belong to the current device;
+ * outputs may not overlap inputs or each other.  Computed in fp32; the same
+ * bits from call to call.  One launch; workspace (B floats) and graphs as for
+ * ce_linear_fwd_bwd.
+ */
+int ce_distill_fwd_bwd(const void *logits, const int32_t *teacher_idx, const void *teacher_val,
+                       const float *teacher_lse, int64_t B, int64_t C, int64_t K, int dtype,
+                       int teacher_dtype, float temperature, int reduction,
+                       const float *grad_scale, float *loss_out, void *grad_out, void *stream);
+
+/*
  * ce_linear_distill_fwd_bwd -- ce_distill_fwd_bwd for logits z = h W^T that
  * are a vocabulary projection, without keeping them: the divergence from a
  * teacher's top logits, and the gradients of the hidden states and weights.

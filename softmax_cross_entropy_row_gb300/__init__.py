@@ -53,7 +53,8 @@ EXPORTS = ("ce_fwd_bwd", "ce_fwd_bwd_path", "ce_query_plan", "ce_get_device_erro
            "ce_release_workspaces", "ce_status_string", "ce_last_cuda_error",
            "ce_fwd_bwd_noalloc", "ce_fwd_bwd_ex", "ce_fwd_bwd_ex_path", "ce_forward",
            "ce_softmax_fwd", "ce_softmax_fwd_path", "ce_softmax_bwd", "ce_fwd_bwd_host",
-           "ce_fwd_bwd_host_grad", "ce_linear_fwd_bwd", "ce_linear_distill_fwd_bwd")
+           "ce_fwd_bwd_host_grad", "ce_linear_fwd_bwd", "ce_distill_fwd_bwd",
+           "ce_linear_distill_fwd_bwd")
 # Symbols declared in include/ce_testing.h (test hooks).
 TEST_EXPORTS = ("ce_fwd_bwd_test",)
 
@@ -123,6 +124,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     i32, f32 = ctypes.c_int32, ctypes.c_float
     lib.ce_linear_fwd_bwd.argtypes = [vp, vp, vp, i64, i64, i64, ci, i32, ci, vp, vp, vp, vp, vp]
     lib.ce_linear_fwd_bwd.restype = ci
+    lib.ce_distill_fwd_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, f32, ci, vp, vp, vp,
+                                       vp]
+    lib.ce_distill_fwd_bwd.restype = ci
     lib.ce_linear_distill_fwd_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci, f32,
                                               ci, vp, vp, vp, vp, vp]
     lib.ce_linear_distill_fwd_bwd.restype = ci
@@ -449,6 +453,38 @@ def ce_linear_fwd_bwd(hidden, weight, targets, loss_out, dhidden_out=None, dweig
                                  _dtype_code(hidden), int(ignore_index), int(reduction),
                                  _ptr(grad_scale), _ptr(loss_out), _ptr(dhidden_out),
                                  _ptr(dweight_out), _stream_handle(stream)))
+
+
+def ce_distill_fwd_bwd(logits, teacher_idx, teacher_val, loss_out, grad_out=None, teacher_lse=None,
+                       temperature=1.0, reduction=CE_REDUCE_MEAN, grad_scale=None,
+                       stream=None) -> None:
+    """Distillation from a teacher's top logits: T^2 KL(q || softmax(logits /
+    T)), q the teacher's distribution over its list, and the gradient.
+
+    logits       [B, C] float32, bfloat16 or float16 CUDA tensor
+    teacher_idx  [B, K] int32 classes, -1 where a place is unused
+    teacher_val  [B, K] the teacher's logits (any of the three dtypes)
+    loss_out     float32: one element (mean, sum) or B (none)
+    grad_out     like logits, or None (the loss alone)
+    teacher_lse  [B] float32 logsumexp of the teacher's logits / T over all its
+                 classes, or None (q is normalised over the list)
+    grad_scale   upstream gradient, one float32 (mean, sum) or [B] (none)
+    """
+    lib = load_library()
+    if logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous [B, C] tensor")
+    if grad_out is not None and (grad_out.shape != logits.shape or grad_out.dtype != logits.dtype
+                                 or not grad_out.is_contiguous()):
+        raise ValueError("grad_out must be a contiguous tensor of the logits' shape and dtype")
+    B, C = logits.shape
+    _check_teacher(teacher_idx, teacher_val, teacher_lse, B)
+    _check_heads(B, reduction, loss_out, grad_scale, logits=logits, teacher_idx=teacher_idx,
+                 teacher_val=teacher_val, teacher_lse=teacher_lse, grad_out=grad_out)
+    _check(lib.ce_distill_fwd_bwd(_ptr(logits), _ptr(teacher_idx), _ptr(teacher_val),
+                                  _ptr(teacher_lse), B, C, teacher_idx.shape[1],
+                                  _dtype_code(logits), _dtype_code(teacher_val),
+                                  float(temperature), int(reduction), _ptr(grad_scale),
+                                  _ptr(loss_out), _ptr(grad_out), _stream_handle(stream)))
 
 
 def ce_linear_distill_fwd_bwd(hidden, weight, teacher_idx, teacher_val, loss_out, dhidden_out=None,

@@ -1,0 +1,457 @@
+// The divergence of a row's softmax from a teacher's top logits, with its
+// gradient (ce_distill_fwd_bwd).  For a row z, temperature T, p = softmax(z /
+// T) and the teacher's probabilities q_k at classes i_k (Q = sum_k q_k),
+//   l    = T^2 sum_k q_k (log q_k - log p_{i_k}),
+//   dz_c = T (Q p_c - sum_{k: i_k = c} q_k).
+// Away from the listed classes the gradient is a multiple of the softmax, so
+// the row is handled like a softmax row and the listed classes are written
+// over it afterwards from their fp32 values.  HBM bound: the row is read once
+// and its gradient written once.
+//
+// A row belongs to a group of G threads: a warp (short rows), a CTA, or a
+// cluster of CTAs (few long rows).  Each thread forms its own maximum and sum
+// of exponentials; the group joins them in a fixed order.  Rows that fit the
+// group's registers stay there; longer ones are read a second time, from L2.
+#include <math.h>
+
+#include <map>
+#include <mutex>
+#include <tuple>
+
+#include "ce_distill.h"
+#include "ce_launch.h"
+
+namespace ce {
+namespace {
+
+__device__ __forceinline__ uint4 ld_row(const uint4 *ptr) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(ptr));
+    return v;
+}
+
+template <typename V>
+__device__ __forceinline__ float value_at(const void *val, long long i) {
+    return Elem<V>::load_global(static_cast<const unsigned char *>(val) + i * Elem<V>::kBytes);
+}
+__device__ __forceinline__ float teacher_at(const DistillParams &p, long long i) {
+    return p.val_dtype == 0   ? value_at<float>(p.val, i)
+           : p.val_dtype == 1 ? value_at<__nv_bfloat16>(p.val, i)
+                              : value_at<__half>(p.val, i);
+}
+
+// A maximum and the sum of 2^((z - m) scale).
+struct MS {
+    float m, s;
+};
+__device__ __forceinline__ MS join(MS a, MS b, float scale) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == -INFINITY) return {m, a.s + b.s};
+    return {m, a.s * ex2((a.m - m) * scale) + b.s * ex2((b.m - m) * scale)};
+}
+
+// The teacher's list of row b, by one warp: classes and log-probabilities to
+// shared memory (unused and bad places: class -1), the mass to *mass, and
+// whether a class was out of range.
+__device__ __forceinline__ void read_list(const DistillParams &p, long long b, int *idx, float *lq,
+                                          float *mass, int *bad) {
+    const int lane = threadIdx.x & 31;
+    const long long i0 = b * p.K;
+    const float inv_t = 1.f / p.temperature;
+    float m = -INFINITY;
+    bool wrong = false;
+    for (int k = lane; k < p.list_words; k += 32) {
+        int c = -1;
+        float t = -INFINITY;
+        if (k < p.K) {
+            c = __ldg(p.idx + i0 + k);
+            if (c < -1 || c >= p.C) {
+                wrong = true;
+                c = -1;
+            }
+            if (c >= 0) t = teacher_at(p, i0 + k);
+        }
+        idx[k] = c;
+        lq[k] = t;
+        m = fmaxf(m, t);
+    }
+    m = warp_max(m);
+    float ref;
+    if (p.lse != nullptr) {
+        ref = __ldg(p.lse + b) - m * inv_t;
+    } else {
+        float s = 0.f;
+        for (int k = lane; k < p.K; k += 32)
+            if (idx[k] >= 0) s += expf((lq[k] - m) * inv_t);
+        ref = logf(warp_sum(s));
+    }
+    float q = 0.f;
+    for (int k = lane; k < p.K; k += 32) {
+        if (idx[k] < 0) continue;
+        const float v = (lq[k] - m) * inv_t - ref;
+        lq[k] = v;
+        q += expf(v);
+    }
+    q = warp_sum(q);
+    wrong = __any_sync(0xffffffffu, wrong);
+    if (lane == 0) {
+        *mass = q;
+        *bad = wrong;
+    }
+}
+
+// A row's place in memory: nh elements up to a 16-byte boundary, nvec whole
+// vectors, the rest; this CTA's share is vectors [v0, v1) and, at the ends,
+// the loose elements: elements [e0, e1).
+struct Span {
+    long long nh, v0, v1, tail0, e0, e1;
+};
+template <typename E>
+__device__ __forceinline__ Span span_of(const unsigned char *row, long long C, int rank, int n) {
+    Span s;
+    const uint32_t ph = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+    s.nh = ph ? min((long long)((16u - ph) / E::kBytes), C) : 0LL;
+    const long long nvec = (C - s.nh) / E::kVec;
+    s.v0 = nvec * rank / n;
+    s.v1 = nvec * (rank + 1) / n;
+    s.tail0 = s.nh + nvec * E::kVec;
+    s.e0 = rank == 0 ? 0 : s.nh + s.v0 * E::kVec;
+    s.e1 = rank == n - 1 ? C : s.nh + s.v1 * E::kVec;
+    return s;
+}
+
+// The loose element of thread t (head, then tail), or -1.
+__device__ __forceinline__ long long loose(const Span &s, long long C, int t) {
+    long long c = -1;
+    if (t < s.nh) c = t;
+    else if (s.tail0 + t - s.nh < C) c = s.tail0 + t - s.nh;
+    return c >= s.e0 && c < s.e1 ? c : -1;
+}
+
+template <typename E, int V>
+__device__ __forceinline__ MS of_vectors(const uint4 (&x)[V], float scale) {
+    typename E::MaxAcc acc = E::max_init();
+#pragma unroll
+    for (int k = 0; k < V; ++k) E::max_step(acc, x[k]);
+    const float m = E::max_value(acc);
+    MS r = {m, 0.f};
+    const float base = m == -INFINITY ? 0.f : m;
+    const unsigned long long nm2 = f2_pack(-base, -base), sc2 = f2_pack(scale, scale);
+    unsigned long long sum = 0ull;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        unsigned long long z[E::kVec / 2];
+        E::unpack2(x[k], z);
+#pragma unroll
+        for (int j = 0; j < E::kVec / 2; ++j) {
+            float a, b;
+            f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), a, b);
+            sum = f2_add(sum, f2_pack(ex2(a), ex2(b)));
+        }
+    }
+    float a, b;
+    f2_unpack(sum, a, b);
+    r.s = a + b;
+    return r;
+}
+
+// The gradient of a vector: 2^((z - m) scale) f.
+template <typename E>
+__device__ __forceinline__ uint4 gradient_of(const uint4 &x, float m, float scale, float f) {
+    unsigned long long z[E::kVec / 2];
+    const unsigned long long nm2 = f2_pack(-m, -m), sc2 = f2_pack(scale, scale),
+                             f2 = f2_pack(f, f);
+    E::unpack2(x, z);
+#pragma unroll
+    for (int j = 0; j < E::kVec / 2; ++j) {
+        float a, b;
+        f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), a, b);
+        z[j] = f2_mul(f2_pack(ex2(a), ex2(b)), f2);
+    }
+    return E::pack2(z);
+}
+
+template <typename E>
+__device__ __forceinline__ void put_vector(unsigned char *g, const uint4 &v, bool aligned) {
+    if (aligned) {
+        __stcs(reinterpret_cast<uint4 *>(g), v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < E::kVec; ++j) E::store(g + j * E::kBytes, element_of<E>(v, j));
+    }
+}
+
+// CTAs per SM the registers are set for: a thread keeps V vectors of its row.
+constexpr int min_ctas(int g, int v, bool loop) {
+    return loop ? 2 : g == 128 ? 4 : g == 32 && v == 8 ? 3 : 2;
+}
+
+template <typename T, int G, int V, bool LOOP>
+__global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) distill_kernel(DistillParams p, int cluster) {
+    using E = Elem<T>;
+    constexpr int ES = E::kBytes;
+    constexpr int NT = G == 32 ? 256 : G;
+    constexpr int GROUPS = NT / G;
+    constexpr int WARPS = G / 32;
+    extern __shared__ unsigned char lists[];
+    __shared__ MS part[2][WARPS * GROUPS];
+    __shared__ float lpart[2][WARPS * GROUPS];
+    __shared__ float4 mine[2];  // this CTA's share, read by the cluster
+    __shared__ float masses[2][GROUPS];
+    __shared__ int bads[2][GROUPS];
+    __shared__ int tail_flag;
+    __shared__ float2 tail_scratch[kTailWarps];
+
+    const int group = threadIdx.x / G;
+    const int t = threadIdx.x % G;
+    const int warp = t >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+    const long long first = (long long)(blockIdx.x / cluster) * GROUPS + group;
+    const long long step = (long long)(gridDim.x / cluster) * GROUPS;
+    const float scale = p.exp_scale;
+    auto group_sync = [] {
+        if constexpr (G == 32) __syncwarp();
+        else __syncthreads();
+    };
+
+    pdl_trigger();
+    pdl_wait();
+
+    const float scalar = scalar_grad_scale(p);
+    int buf = 0;
+    for (long long b = first; b < p.B; b += step, buf ^= 1) {
+        const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
+        const Span sp = span_of<E>(row, p.C, rank, cluster);
+        const uint4 *vp = reinterpret_cast<const uint4 *>(row + sp.nh * ES);
+        const uint4 kNeg = make_uint4(E::kNegInfWord, E::kNegInfWord, E::kNegInfWord,
+                                      E::kNegInfWord);
+        uint4 x[V];
+        auto load = [&](long long v) {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                x[k] = v + k * G + t < sp.v1 ? ld_row(vp + v + k * G + t) : kNeg;
+        };
+        if constexpr (!LOOP) load(sp.v0);
+        const long long lc = loose(sp, p.C, t);
+        const float lz = lc >= 0 ? E::load_global(row + lc * ES) : -INFINITY;
+
+        int *idx = reinterpret_cast<int *>(lists) + (buf * GROUPS + group) * 2 * p.list_words;
+        float *lq = reinterpret_cast<float *>(idx + p.list_words);
+        if (warp == 0) read_list(p, b, idx, lq, &masses[buf][group], &bads[buf][group]);
+
+        // this thread's maximum and sum
+        MS a = {lz, lz == -INFINITY ? 0.f : lz == lz ? 1.f : lz};
+        if constexpr (LOOP) {
+            for (long long v = sp.v0; v < sp.v1; v += (long long)V * G) {
+                load(v);
+                a = join(a, of_vectors<E, V>(x, scale), scale);
+            }
+        } else {
+            a = join(a, of_vectors<E, V>(x, scale), scale);
+        }
+        // the warp's, the group's, the cluster's
+        const float wm = warp_max(a.m);
+        a.s = warp_sum(wm == -INFINITY ? a.s : a.s * ex2((a.m - wm) * scale));
+        a.m = wm;
+        if constexpr (G > 32) {
+            if (lane == 0) part[buf][warp] = a;
+            __syncthreads();
+            a = part[buf][0];
+#pragma unroll
+            for (int i = 1; i < WARPS; ++i) a = join(a, part[buf][i], scale);
+            if (cluster > 1) {
+                if (threadIdx.x == 0) mine[buf] = make_float4(a.m, a.s, 0.f, 0.f);
+                cluster_sync();
+                a = {-INFINITY, 0.f};
+                for (int i = 0; i < cluster; ++i) {
+                    const float4 v = ld_dsmem_f4(&mine[buf], i);
+                    a = join(a, {v.x, v.y}, scale);
+                }
+            }
+        } else {
+            __syncwarp();
+        }
+        const float m = a.m, S = a.s;
+        const float mass = masses[buf][group];
+        const float f = row_grad_factor(p, scalar, b) * p.temperature;
+        const float inv = 1.f / S;
+
+        if (writes_grad(p)) {
+            unsigned char *grow = p.grad + (size_t)(b * p.C) * ES;
+            unsigned char *gv = grow + sp.nh * ES;
+            const bool zero = mass == 0.f;  // no list: nothing to learn, whatever the row holds
+            const float fs = zero ? 0.f : mass * inv * f;
+            if (lc >= 0) E::store(grow + lc * ES, zero ? 0.f : ex2((lz - m) * scale) * fs);
+            auto write = [&](long long v) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const long long i = v + k * G + t;
+                    if (i < sp.v1)
+                        put_vector<E>(gv + i * 16,
+                                      zero ? make_uint4(0u, 0u, 0u, 0u)
+                                           : gradient_of<E>(x[k], m, scale, fs),
+                                      p.grad_vec_ok);
+                }
+            };
+            if constexpr (LOOP) {
+                for (long long v = sp.v0; v < sp.v1; v += (long long)V * G) {
+                    load(v);
+                    write(v);
+                }
+            } else {
+                write(sp.v0);
+            }
+            group_sync();
+        }
+
+        // the listed classes, and the loss
+        const float log2S = log2f(S);
+        float l = 0.f;
+        for (int k = t; k < p.K; k += G) {
+            const int c = idx[k];
+            if (c < 0) continue;
+            const bool here = c >= sp.e0 && c < sp.e1;
+            if (!here && rank != 0) continue;
+            const float lp2 = (E::load_global(row + (size_t)c * ES) - m) * scale - log2S;
+            const float v = lq[k];
+            const float q = expf(v);
+            if (q != 0.f) l += q * (v - kLn2 * lp2);
+            if (!writes_grad(p) || !here) continue;
+            float all = 0.f;
+            bool mine_first = true;
+            for (int j = 0; j < p.list_words; j += 4) {
+                const int4 o = *reinterpret_cast<const int4 *>(idx + j);
+                const int oc[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (oc[i] != c) continue;
+                    if (j + i < k) mine_first = false;
+                    all += expf(lq[j + i]);
+                }
+            }
+            if (mine_first)
+                E::store(p.grad + (size_t)(b * p.C + c) * ES,
+                         mass == 0.f ? 0.f : (mass * ex2(lp2) - all) * f);
+        }
+        if (rank == 0) {
+            l = warp_sum(l);
+            if constexpr (G > 32) {
+                if (lane == 0) lpart[buf][warp] = l;
+                __syncthreads();
+                l = lpart[buf][0];
+                for (int i = 1; i < WARPS; ++i) l += lpart[buf][i];
+            }
+            if (t == 0) {
+                l *= p.temperature * p.temperature;
+                if (mass == 0.f) l = 0.f;
+                if (bads[buf][group]) {
+                    l = NAN;
+                    atomicAdd(&p.err[kErrBadTarget], 1);
+                }
+                p.loss_rows[b] = l;
+            }
+        }
+    }
+    if (cluster > 1) cluster_sync();  // no CTA leaves while a peer may read its share
+    finish_cta(p, &tail_flag, tail_scratch);
+}
+
+// The builds: a warp per row of up to 8 KB; a CTA per row held in registers
+// up to 64 KB; longer rows in two passes.
+template <typename T>
+const void *kernel_of(const DistillPlan &pl) {
+    if (pl.loop) return reinterpret_cast<const void *>(distill_kernel<T, 512, 8, true>);
+    if (pl.group == 32 && pl.vecs == 8)
+        return reinterpret_cast<const void *>(distill_kernel<T, 32, 8, false>);
+    if (pl.group == 32) return reinterpret_cast<const void *>(distill_kernel<T, 32, 16, false>);
+    if (pl.group == 128) return reinterpret_cast<const void *>(distill_kernel<T, 128, 16, false>);
+    return reinterpret_cast<const void *>(distill_kernel<T, 256, 16, false>);
+}
+const void *kernel_of(int dtype, const DistillPlan &pl) {
+    return dtype == 0   ? kernel_of<float>(pl)
+           : dtype == 1 ? kernel_of<__nv_bfloat16>(pl)
+                        : kernel_of<__half>(pl);
+}
+
+int threads_of(const DistillPlan &pl) { return pl.group == 32 ? 256 : pl.group; }
+
+// Resident CTAs per SM, remembered (a captured call then asks nothing).
+cudaError_t resident(const void *f, int threads, int smem, int *n) {
+    static std::mutex mu;
+    static std::map<std::tuple<int, const void *, int>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    int &v = known[{dev, f, smem}];
+    if (v == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, f, threads, smem);
+        if (e != cudaSuccess) return e;
+    }
+    *n = v;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
+                         DistillPlan *pl) {
+    const long long row = C * (dtype == 0 ? 4 : 2);
+    DistillPlan r = {};
+    r.cluster = 1;
+    r.vecs = 16;
+    if (row <= 8192) {
+        r.group = 32;
+        if (row <= 4096) r.vecs = 8;
+    } else {
+        // few rows: up to 8 CTAs each, as long as every SM then has one
+        while (r.cluster < 8 && B * r.cluster * 2 <= sms && row / r.cluster > 16384) r.cluster *= 2;
+        const long long share = row / r.cluster;
+        r.group = share <= 128LL * 16 * 16 ? 128 : 256;
+        if (share > 256LL * 16 * 16) {
+            r.loop = true;
+            r.group = 512;
+            r.vecs = 8;
+        }
+    }
+    const int groups = r.group == 32 ? 8 : 1;
+    r.smem = 2 * groups * 2 * ((K + 3) / 4 * 4) * 4;
+    const void *f = kernel_of(dtype, r);
+    cudaError_t e = ensure_smem_attr(f, r.smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    if ((e = resident(f, threads_of(r), r.smem, &per_sm)) != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const long long want = (B + groups - 1) / groups * r.cluster;
+    const long long most = (long long)per_sm * sms / r.cluster * r.cluster;
+    r.ctas = (int)(want < most ? want : most);
+    *pl = r;
+    return cudaSuccess;
+}
+
+cudaError_t launch_distill(const DistillParams &p, int dtype, const DistillPlan &pl,
+                           cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.ctas, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads_of(pl), 1, 1);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)pl.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pl.cluster > 1 ? 2 : 1;
+    DistillParams q = p;
+    int cluster = pl.cluster;
+    void *args[] = {&q, &cluster};
+    return cudaLaunchKernelExC(&cfg, kernel_of(dtype, pl), args);
+}
+
+}  // namespace ce

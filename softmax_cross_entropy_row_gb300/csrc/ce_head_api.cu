@@ -1,5 +1,6 @@
-// C-ABI of the vocabulary projection's operators (ce_linear_fwd_bwd,
-// ce_linear_distill_fwd_bwd in include/ce.h): argument checks, workspaces, the
+// C-ABI of the vocabulary projection's and the teacher's operators
+// (ce_linear_fwd_bwd, ce_distill_fwd_bwd, ce_linear_distill_fwd_bwd in
+// include/ce.h): argument checks, workspaces, the
 // tensor maps of the operands and the sequence of launches.  Nothing here
 // computes on the host.
 #include <cuda.h>
@@ -14,6 +15,7 @@
 #include <vector>
 
 #include "../../include/ce.h"
+#include "ce_distill.h"
 #include "ce_head_gemm.h"
 #include "ce_head_rows.h"
 #include "ce_host.h"
@@ -114,6 +116,7 @@ int tensor_map(CUtensorMap *map, int dtype, const void *base, long long rows, lo
 
 // ------------------------------------------------------------------ plans
 
+constexpr size_t kTicketOffset = 128;          // within the workspace's first 256 bytes
 constexpr long long kMaxK = 1024;             // places of a teacher's list
 constexpr long long kPieceBytes = 1LL << 30;  // kept exponentials, see rows_per_piece
 
@@ -469,6 +472,99 @@ int run(const Call &c) {
     return CE_OK;
 }
 
+// The teacher's divergence on given logits: one launch.
+struct DistillCall {
+    const void *logits;
+    const int32_t *idx;
+    const void *val;
+    const float *lse;
+    int64_t B, C, K;
+    int dtype, teacher_dtype;
+    float temperature;
+    int reduction;
+    const float *scale;
+    float *loss;
+    void *grad, *stream;
+};
+
+int check(const DistillCall &c) {
+    for (int t : {c.dtype, c.teacher_dtype})
+        if (t != CE_F32 && t != CE_BF16 && t != CE_F16) return CE_ERR_DTYPE;
+    if (c.reduction != CE_REDUCE_MEAN && c.reduction != CE_REDUCE_SUM &&
+        c.reduction != CE_REDUCE_NONE)
+        return CE_ERR_REDUCTION;
+    if (!c.logits || !c.idx || !c.val || !c.loss) return CE_ERR_NULL;
+    const uintptr_t es = c.dtype == CE_F32 ? 4 : 2, te = c.teacher_dtype == CE_F32 ? 4 : 2;
+    if (c.B < 1 || c.C < 1 || c.K < 1 || c.K > kMaxK || c.B > 0x7fffffffLL || c.C > 0x7fffffffLL ||
+        (unsigned long long)c.B * (unsigned long long)c.C > (1ull << 61) / es)
+        return CE_ERR_SHAPE;
+    if (!(c.temperature > 0.f && isfinite(c.temperature))) return CE_ERR_TEMPERATURE;
+    const auto off = [](const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a; };
+    if (off(c.logits, es) || off(c.grad, es) || off(c.idx, 4) || off(c.val, te) || off(c.lse, 4) ||
+        off(c.scale, 4) || off(c.loss, 4))
+        return CE_ERR_ALIGN;
+    const size_t rows = c.reduction == CE_REDUCE_NONE ? (size_t)c.B * 4 : 4;
+    const size_t zb = (size_t)c.B * c.C * es;
+    const std::pair<const void *, size_t> in[] = {{c.logits, zb},
+                                                  {c.idx, (size_t)c.B * c.K * 4},
+                                                  {c.val, (size_t)c.B * c.K * te},
+                                                  {c.lse, (size_t)c.B * 4},
+                                                  {c.scale, rows}};
+    for (const auto &r : in)
+        if (ce::host_overlap(c.loss, rows, r.first, r.second) ||
+            ce::host_overlap(c.grad, zb, r.first, r.second))
+            return CE_ERR_OVERLAP;
+    return ce::host_overlap(c.loss, rows, c.grad, zb) ? CE_ERR_OVERLAP : CE_OK;
+}
+
+int run(const DistillCall &c) {
+    CE_TRY(check(c));
+    int dev = 0, sms = 0;
+    CE_TRY(ce::host_device(&dev, &sms));
+    for (const void *p : {c.logits, (const void *)c.idx, c.val, (const void *)c.lse,
+                          (const void *)c.scale, (const void *)c.loss, (const void *)c.grad})
+        if (p) CE_TRY(ce::host_check_device_pointer(p, dev));
+    cudaStream_t s = static_cast<cudaStream_t>(c.stream);
+    ce::DistillParams p;
+    CE_TRY(ce::host_error_counters(dev, s, &p.err));
+    ce::DistillPlan plan;
+    CE_CUDA(ce::plan_distill(c.B, c.C, (int)c.K, c.dtype, c.grad != nullptr, sms, &plan));
+
+    const bool none = c.reduction == CE_REDUCE_NONE;
+    std::lock_guard<std::mutex> lk(g_mu);
+    unsigned char *ws = nullptr;
+    CE_TRY(workspace(dev, s, 256 + (none ? 0 : (size_t)round_up(c.B, 1024) * 4), &ws));
+    p.logits = static_cast<const unsigned char *>(c.logits);
+    p.targets = nullptr;
+    p.grad = static_cast<unsigned char *>(c.grad);
+    p.loss_out = c.loss;
+    p.loss_rows = none ? c.loss : reinterpret_cast<float *>(ws + 256);
+    p.ticket = reinterpret_cast<unsigned int *>(ws + kTicketOffset);
+    p.parts = nullptr;
+    p.zt = nullptr;
+    p.B = c.B;
+    p.C = c.C;
+    p.inv_b = (float)(1.0 / (double)c.B);
+    p.lo_clip = p.hi_clip = 0;
+    p.grad_vec_ok = c.grad != nullptr && (reinterpret_cast<uintptr_t>(c.grad) -
+                                          reinterpret_cast<uintptr_t>(c.logits)) % 16 == 0;
+    p.reduction = c.reduction;
+    p.grad_base = c.reduction == CE_REDUCE_MEAN ? p.inv_b : 1.f;
+    p.grad_scale = c.scale;
+    p.scale_per_row = c.scale != nullptr && none;
+    p.softmax = 0;
+    p.idx = c.idx;
+    p.val = c.val;
+    p.val_dtype = c.teacher_dtype;
+    p.lse = c.lse;
+    p.K = (int)c.K;
+    p.list_words = (int)round_up(c.K, 4);
+    p.temperature = c.temperature;
+    p.exp_scale = ce::kLog2e / c.temperature;
+    CE_CUDA(ce::launch_distill(p, c.dtype, plan, s));
+    return CE_OK;
+}
+
 }  // namespace
 
 namespace ce {
@@ -516,6 +612,29 @@ int ce_linear_fwd_bwd(const void *hidden, const void *weight, const int32_t *tar
     c.loss = loss_out;
     c.dhidden = dhidden_out;
     c.dweight = dweight_out;
+    c.stream = stream;
+    return run(c);
+}
+
+int ce_distill_fwd_bwd(const void *logits, const int32_t *teacher_idx, const void *teacher_val,
+                       const float *teacher_lse, int64_t B, int64_t C, int64_t K, int dtype,
+                       int teacher_dtype, float temperature, int reduction,
+                       const float *grad_scale, float *loss_out, void *grad_out, void *stream) {
+    DistillCall c = {};
+    c.logits = logits;
+    c.idx = teacher_idx;
+    c.val = teacher_val;
+    c.lse = teacher_lse;
+    c.B = B;
+    c.C = C;
+    c.K = K;
+    c.dtype = dtype;
+    c.teacher_dtype = teacher_dtype;
+    c.temperature = temperature;
+    c.reduction = reduction;
+    c.scale = grad_scale;
+    c.loss = loss_out;
+    c.grad = grad_out;
     c.stream = stream;
     return run(c);
 }
