@@ -359,10 +359,346 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
     finish_cta(p, &tail_flag, tail_scratch);
 }
 
-// The builds: a warp per row of up to 8 KB; a CTA per row held in registers
-// up to 64 KB; longer rows in two passes.
+// ------------------------------------------------------------------- ring
+//
+// Many long rows: a CTA takes one row at a time, streamed through a ring of
+// shared-memory chunks by a warp of its own (TMA bulk copies), while another
+// warp reads the teacher's lists a row ahead.  RESIDENT: the ring holds a row,
+// whose chunks stay for the gradient; otherwise the row is streamed a second
+// time, from L2.  The next row's copies are under way while a row is reduced,
+// and one barrier per row holds all warps: the listed classes are written by
+// one warp (another one each row) after the others have passed their stores,
+// without their waiting for it.
+__host__ __device__ constexpr int ring_vecs(int nt) { return nt == 512 ? 4 : 2; }  // per thread and chunk
+__host__ __device__ constexpr int chunk_bytes(int nt) { return nt * 16 * ring_vecs(nt); }
+constexpr int kMaxSlots = 16;
+constexpr int kRingWarps = 2;  // the copying warp and the list warp
+
+// Classes of a list with their places added up, by one warp: cls[k] the class
+// of place k and prob[k] its probability with those of its later places, or
+// cls[k] = -1 (unused, or an earlier place has the class).  Returns
+// sum_k q_k log q_k.  A hash table (`table`, 2^bits >= 2 words) finds out
+// whether any class is listed twice; the sums run in the list's order.
+__device__ __forceinline__ float merge_list(const int *idx, const float *lq, int words, int *cls,
+                                            float *prob, int *table, int bits) {
+    const int lane = threadIdx.x & 31;
+    const int size = 1 << bits;
+    for (int i = lane; i < size; i += 32) table[i] = -1;
+    __syncwarp();
+    bool twice = false;
+    float h = 0.f;
+    for (int k = lane; k < words; k += 32) {
+        const int c = idx[k];
+        float q = 0.f;
+        if (c >= 0) {
+            const float v = lq[k];
+            q = expf(v);
+            if (q != 0.f) h += q * v;
+            unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
+            for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
+                const int was = atomicCAS(&table[at], -1, c);
+                twice |= was == c;
+                if (was == -1 || was == c) break;
+                at = (at + 1) & (size - 1);
+            }
+        }
+        cls[k] = c;
+        prob[k] = q;
+    }
+    if (__any_sync(0xffffffffu, twice)) {
+        __syncwarp();
+        for (int k = lane; k < words; k += 32) {
+            const int c = idx[k];
+            if (c < 0) continue;
+            float q = 0.f;
+            bool first = true;
+            for (int j = 0; j < words; ++j) {
+                if (idx[j] != c) continue;
+                if (j < k) first = false;
+                q += expf(lq[j]);
+            }
+            cls[k] = first ? c : -1;
+            prob[k] = q;
+        }
+    }
+    return warp_sum(h);
+}
+
+struct RingShape {
+    int slots;
+    int table_bits;
+};
+
+// Shared memory of the lists: idx, lq (being read), two of (cls, prob), table.
+__host__ __device__ constexpr int list_bytes(int words, int bits) {
+    return words * 4 * 6 + (4 << bits);
+}
+
+template <typename T, int NT, bool RESIDENT>
+__global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
+    distill_ring_kernel(DistillParams p, RingShape rs) {
+    using E = Elem<T>;
+    constexpr int ES = E::kBytes;
+    constexpr int V = ring_vecs(NT);
+    constexpr int CH = chunk_bytes(NT);
+    constexpr int VC = CH / 16;
+    constexpr int NW = NT / 32;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+    __shared__ uint64_t list_full[2], list_empty[2];
+    __shared__ MS part[2][NW];
+    __shared__ int fine[2][NW];  // the warp's waits have all been met
+    __shared__ float masses[2], negent[2];
+    __shared__ int bads[2];
+    __shared__ int dead;  // a wait gave up
+    __shared__ int tail_flag;
+    __shared__ float2 tail_scratch[kTailWarps];
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int S = rs.slots;
+    const int words = p.list_words;
+    int *idx = reinterpret_cast<int *>(ring + (size_t)S * CH);
+    float *lq = reinterpret_cast<float *>(idx + words);
+    int *table = idx + 6 * words;
+    auto cls_of = [&](int b) { return idx + 2 * words + b * 2 * words; };
+    auto prob_of = [&](int b) { return reinterpret_cast<float *>(idx + 3 * words + b * 2 * words); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], NW);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&list_full[i], 1);
+            mbar_init(&list_empty[i], 1);
+        }
+        dead = 0;
+        fence_mbar_init();
+    }
+    pdl_trigger();
+    __syncthreads();
+    pdl_wait();
+
+    auto fail = [&] {
+        *reinterpret_cast<volatile int *>(&dead) = 1;
+        atomicAdd(&p.err[kErrTimeout], 1);
+    };
+    auto is_dead = [&] { return *reinterpret_cast<volatile int *>(&dead) != 0; };
+    const float scale = p.exp_scale;
+    const bool grads = writes_grad(p);
+    const int passes = grads && !RESIDENT ? 2 : 1;
+
+    if (warp == NW) {
+        // ---- the copies
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            const uint64_t keep = l2_policy_evict_last(), drop = l2_policy_evict_first();
+            for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
+                const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
+                const Span sp = span_of<E>(row, p.C, 0, 1);
+                const unsigned char *v0 = row + sp.nh * ES;
+                for (int pass = 0; pass < passes; ++pass) {
+                    const uint64_t policy = pass + 1 < passes ? keep : drop;
+                    for (long long v = 0; v < sp.v1; v += VC) {
+                        if (!mbar_wait(&empty[s], ph ^ 1u)) {
+                            fail();
+                            goto copied;
+                        }
+                        const uint32_t bytes = (uint32_t)min((long long)VC, sp.v1 - v) * 16u;
+                        mbar_arrive_expect_tx(&full[s], bytes);
+                        bulk_g2s_hint(ring + (size_t)s * CH, v0 + v * 16, bytes, &full[s], policy);
+                        ++issued;
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            }
+        copied:
+            if (is_dead()) {  // what is in flight lands before shared memory is given up
+                for (int n = min(issued, S); n > 0; --n) {
+                    if (s == 0) {
+                        s = S;
+                        ph ^= 1u;
+                    }
+                    --s;
+                    mbar_wait(&full[s], ph);
+                }
+            }
+        }
+    } else if (warp == NW + 1) {
+        // ---- the lists
+        uint32_t ph = 0;
+        int lb = 0;
+        for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&list_empty[lb], ph ^ 1u))) {
+                if (lane == 0) fail();
+                break;
+            }
+            read_list(p, b, idx, lq, &masses[lb], &bads[lb]);
+            __syncwarp();
+            const float h = merge_list(idx, lq, words, cls_of(lb), prob_of(lb), table, rs.table_bits);
+            if (lane == 0) negent[lb] = h;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&list_full[lb]);
+            lb ^= 1;
+            if (lb == 0) ph ^= 1u;
+        }
+    } else {
+        // ---- the rows
+        const int t = threadIdx.x;
+        const float scalar = scalar_grad_scale(p);
+        int s = 0, buf = 0, turn = 0;
+        uint32_t ph = 0, lph = 0;
+        // A wait that gave up ends the warp's part in this row; the CTA stops
+        // at its next barrier, where all warps see the same flags.
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
+            return ok;
+        };
+        for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
+            const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
+            const Span sp = span_of<E>(row, p.C, 0, 1);
+            const long long lc = loose(sp, p.C, t);
+            const float lz = lc >= 0 ? E::load_global(row + lc * ES) : -INFINITY;
+            MS a = {lz, lz == -INFINITY ? 0.f : lz == lz ? 1.f : lz};
+            auto fetch = [&](int slot, long long v, uint4 (&x)[V]) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int i = k * NT + t;
+                    x[k] = v + i < sp.v1 ? lds128(ring + (size_t)slot * CH + i * 16)
+                                         : make_uint4(E::kNegInfWord, E::kNegInfWord,
+                                                      E::kNegInfWord, E::kNegInfWord);
+                }
+            };
+            auto release = [&](int slot) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
+            };
+            const int s0 = s;
+            for (long long v = 0; v < sp.v1; v += VC) {
+                if (wait(&full[s], ph)) {
+                    uint4 x[V];
+                    fetch(s, v, x);
+                    a = join(a, of_vectors<E, V>(x, scale), scale);
+                    if (!RESIDENT || !grads) release(s);
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!wait(&list_full[buf], lph) && lane == 0) fail();
+            const float wm = warp_max(a.m);
+            a.s = warp_sum(wm == -INFINITY ? a.s : a.s * ex2((a.m - wm) * scale));
+            if (lane == 0) {
+                part[buf][warp] = {wm, a.s};
+                fine[buf][warp] = ok;
+            }
+            named_sync(1, NT);
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) all = all && fine[buf][i];
+            if (!all) break;
+            a = part[buf][0];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) a = join(a, part[buf][i], scale);
+            const float m = a.m;
+            const float inv = 1.f / a.s;
+            const float mass = masses[buf];
+            const float f = row_grad_factor(p, scalar, b) * p.temperature;
+            const bool mine = warp == turn;
+            if (++turn == NW) turn = 0;
+            if (grads) {
+                unsigned char *grow = p.grad + (size_t)(b * p.C) * ES;
+                unsigned char *gv = grow + sp.nh * ES;
+                const bool zero = mass == 0.f;  // no list: nothing to learn, whatever the row holds
+                const float fs = zero ? 0.f : mass * inv * f;
+                if (lc >= 0) E::store(grow + lc * ES, zero ? 0.f : ex2((lz - m) * scale) * fs);
+                int r = RESIDENT ? s0 : s;
+                for (long long v = 0; v < sp.v1; v += VC) {
+                    if (!RESIDENT) wait(&full[r], ph);
+                    if (ok) {
+                        uint4 x[V];
+                        fetch(r, v, x);
+                        release(r);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) {
+                            const long long i = v + k * NT + t;
+                            if (i < sp.v1)
+                                put_vector<E>(gv + i * 16,
+                                              zero ? make_uint4(0u, 0u, 0u, 0u)
+                                                   : gradient_of<E>(x[k], m, scale, fs),
+                                              p.grad_vec_ok);
+                        }
+                    }
+                    if (++r == S) {
+                        r = 0;
+                        if (!RESIDENT) ph ^= 1u;
+                    }
+                }
+                if (!RESIDENT) s = r;
+                if (!ok && lane == 0) fail();
+                // the listed classes go over these stores
+                if (mine)
+                    named_sync(2, NT);
+                else
+                    named_arrive(2, NT);
+            }
+            if (mine) {
+                const int *cls = cls_of(buf);
+                const float *prob = prob_of(buf);
+                const float log2S = log2f(a.s);
+                float cross = 0.f;
+                for (int k = lane; k < words; k += 32) {
+                    const int c = cls[k];
+                    if (c < 0) continue;
+                    const float lp2 = (E::load_global(row + (size_t)c * ES) - m) * scale - log2S;
+                    const float q = prob[k];
+                    if (q != 0.f) cross += q * lp2;
+                    if (grads)
+                        E::store(p.grad + (size_t)(b * p.C + c) * ES,
+                                 mass == 0.f ? 0.f : (mass * ex2(lp2) - q) * f);
+                }
+                cross = warp_sum(cross);
+                if (lane == 0) {
+                    float l = (negent[buf] - kLn2 * cross) * p.temperature * p.temperature;
+                    if (mass == 0.f) l = 0.f;
+                    if (bads[buf]) {
+                        l = NAN;
+                        atomicAdd(&p.err[kErrBadTarget], 1);
+                    }
+                    p.loss_rows[b] = l;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&list_empty[buf]);
+            }
+            buf ^= 1;
+            if (buf == 0) lph ^= 1u;
+        }
+    }
+    __syncthreads();
+    if (is_dead()) {  // every row whose result is in doubt reads NaN
+        if (threadIdx.x == 0)
+            for (long long b = blockIdx.x; b < p.B; b += gridDim.x) p.loss_rows[b] = NAN;
+        __syncthreads();
+    }
+    finish_cta(p, &tail_flag, tail_scratch);
+}
+
+// The builds: a warp per row of up to 8 KB; the ring, its row resident or
+// streamed twice; for few rows a CTA or a cluster per row, in registers or in
+// two passes.
 template <typename T>
 const void *kernel_of(const DistillPlan &pl) {
+    if (pl.ring_threads == 256)
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 256, true>);
+    if (pl.ring_threads == 512)
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, false>);
     if (pl.loop) return reinterpret_cast<const void *>(distill_kernel<T, 512, 8, true>);
     if (pl.group == 32 && pl.vecs == 8)
         return reinterpret_cast<const void *>(distill_kernel<T, 32, 8, false>);
@@ -376,7 +712,10 @@ const void *kernel_of(int dtype, const DistillPlan &pl) {
                         : kernel_of<__half>(pl);
 }
 
-int threads_of(const DistillPlan &pl) { return pl.group == 32 ? 256 : pl.group; }
+int threads_of(const DistillPlan &pl) {
+    if (pl.ring_threads) return pl.ring_threads + 32 * kRingWarps;
+    return pl.group == 32 ? 256 : pl.group;
+}
 
 // Resident CTAs per SM, remembered (a captured call then asks nothing).
 cudaError_t resident(const void *f, int threads, int smem, int *n) {
@@ -396,6 +735,11 @@ cudaError_t resident(const void *f, int threads, int smem, int *n) {
 }
 
 }  // namespace
+
+// Shared memory of an SM, and what a CTA of the ring needs beside the ring
+// and its lists (the system's 1 KB and the kernel's static part).
+constexpr int kSmemPerSm = 228 * 1024;
+constexpr int kSmemReserve = 2048;
 
 cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
                          DistillPlan *pl) {
@@ -417,8 +761,23 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
             r.vecs = 8;
         }
     }
+    const int words = (K + 3) / 4 * 4;
+    if (row > 8192 && B > sms) {
+        // the ring: a row resident in the smaller one (two CTAs per SM) if it
+        // takes no more than its bytes, else streamed twice (one CTA per SM)
+        r.table_bits = 1;
+        while ((1 << r.table_bits) < 2 * words) ++r.table_bits;
+        const int lists = list_bytes(words, r.table_bits);
+        const int two = (kSmemPerSm / 2 - kSmemReserve - lists) / chunk_bytes(256);
+        const bool resident = row <= (long long)two * chunk_bytes(256);
+        r.cluster = 1;
+        r.ring_threads = resident ? 256 : 512;
+        const int room = resident ? two : (kSmemPerSm - kSmemReserve - lists) / chunk_bytes(512);
+        r.slots = room < kMaxSlots ? room : kMaxSlots;
+        r.smem = r.slots * chunk_bytes(r.ring_threads) + lists;
+    }
     const int groups = r.group == 32 ? 8 : 1;
-    r.smem = 2 * groups * 2 * ((K + 3) / 4 * 4) * 4;
+    if (!r.ring_threads) r.smem = 2 * groups * 2 * words * 4;
     const void *f = kernel_of(dtype, r);
     cudaError_t e = ensure_smem_attr(f, r.smem);
     if (e != cudaSuccess) return e;
@@ -450,7 +809,8 @@ cudaError_t launch_distill(const DistillParams &p, int dtype, const DistillPlan 
     cfg.numAttrs = pl.cluster > 1 ? 2 : 1;
     DistillParams q = p;
     int cluster = pl.cluster;
-    void *args[] = {&q, &cluster};
+    RingShape ring = {pl.slots, pl.table_bits};
+    void *args[] = {&q, pl.ring_threads ? static_cast<void *>(&ring) : &cluster};
     return cudaLaunchKernelExC(&cfg, kernel_of(dtype, pl), args);
 }
 

@@ -53,10 +53,12 @@ def check_distill(z, idx, val, dtype, lse=None, T=1.0, reduction=MEAN, scale=Non
 
 # (B, C, K): a warp per row (one class, ragged, 4 and 8 KB rows), a CTA per
 # row (both sizes), two passes, and few long rows on a cluster of CTAs (each
-# of the cluster's sizes, and too long for its registers)
+# of the cluster's sizes, and too long for its registers); then many rows
+# through the ring (resident, its fullest row, streamed twice, a long list)
 SHAPES = [(1, 1, 1), (5, 7, 3), (300, 1000, 8), (17, 2047, 33), (9, 4096, 1), (3, 9001, 64),
-          (400, 16000, 100), (330, 32000, 64), (320, 50257, 20), (40, 50257, 7), (2, 128256, 100),
-          (1, 300001, 1024), (30, 131072, 256)]
+          (100, 16000, 100), (400, 16000, 100), (330, 32000, 64), (320, 50257, 20), (40, 50257, 7), (2, 128256, 100),
+          (1, 300001, 1024), (30, 131072, 256),
+          (700, 9001, 31), (320, 53248, 5), (310, 53264, 64), (200, 130001, 1024)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
