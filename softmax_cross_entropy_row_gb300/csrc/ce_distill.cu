@@ -62,17 +62,16 @@ __device__ __forceinline__ void read_list(const DistillParams &p, long long b, i
     const float inv_t = 1.f / p.temperature;
     float m = -INFINITY;
     bool wrong = false;
+#pragma unroll 4
     for (int k = lane; k < p.list_words; k += 32) {
-        int c = -1;
-        float t = -INFINITY;
-        if (k < p.K) {
-            c = __ldg(p.idx + i0 + k);
-            if (c < -1 || c >= p.C) {
-                wrong = true;
-                c = -1;
-            }
-            if (c >= 0) t = teacher_at(p, i0 + k);
+        // both loads at once: an unused place's value is read and dropped
+        int c = k < p.K ? __ldg(p.idx + i0 + k) : -1;
+        float t = k < p.K ? teacher_at(p, i0 + k) : -INFINITY;
+        if (c < -1 || c >= p.C) {
+            wrong = true;
+            c = -1;
         }
+        if (c < 0) t = -INFINITY;
         idx[k] = c;
         lq[k] = t;
         m = fmaxf(m, t);
@@ -130,31 +129,35 @@ __device__ __forceinline__ long long loose(const Span &s, long long C, int t) {
     return c >= s.e0 && c < s.e1 ? c : -1;
 }
 
+// V vectors added to a running maximum and sum, which is rescaled when the
+// maximum grows (after a row's first vectors it hardly ever does).
 template <typename E, int V>
-__device__ __forceinline__ MS of_vectors(const uint4 (&x)[V], float scale) {
+__device__ __forceinline__ void add_vectors(MS &a, const uint4 (&x)[V], float scale) {
     typename E::MaxAcc acc = E::max_init();
 #pragma unroll
     for (int k = 0; k < V; ++k) E::max_step(acc, x[k]);
     const float m = E::max_value(acc);
-    MS r = {m, 0.f};
-    const float base = m == -INFINITY ? 0.f : m;
+    if (m > a.m) {
+        a.s *= ex2((a.m - m) * scale);
+        a.m = m;
+    }
+    const float base = a.m == -INFINITY ? 0.f : a.m;
     const unsigned long long nm2 = f2_pack(-base, -base), sc2 = f2_pack(scale, scale);
-    unsigned long long sum = 0ull;
+    unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         unsigned long long z[E::kVec / 2];
         E::unpack2(x[k], z);
 #pragma unroll
         for (int j = 0; j < E::kVec / 2; ++j) {
-            float a, b;
-            f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), a, b);
-            sum = f2_add(sum, f2_pack(ex2(a), ex2(b)));
+            float u, v;
+            f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), u, v);
+            sum[j & 1] = f2_add(sum[j & 1], f2_pack(ex2(u), ex2(v)));
         }
     }
-    float a, b;
-    f2_unpack(sum, a, b);
-    r.s = a + b;
-    return r;
+    float u, v;
+    f2_unpack(f2_add(sum[0], sum[1]), u, v);
+    a.s += u + v;
 }
 
 // The gradient of a vector: 2^((z - m) scale) f.
@@ -247,10 +250,10 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
         if constexpr (LOOP) {
             for (long long v = sp.v0; v < sp.v1; v += (long long)V * G) {
                 load(v);
-                a = join(a, of_vectors<E, V>(x, scale), scale);
+                add_vectors<E, V>(a, x, scale);
             }
         } else {
-            a = join(a, of_vectors<E, V>(x, scale), scale);
+            add_vectors<E, V>(a, x, scale);
         }
         // the warp's, the group's, the cluster's
         const float wm = warp_max(a.m);
@@ -366,13 +369,14 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
 // warp reads the teacher's lists a row ahead.  RESIDENT: the ring holds a row,
 // whose chunks stay for the gradient; otherwise the row is streamed a second
 // time, from L2.  The next row's copies are under way while a row is reduced,
-// and one barrier per row holds all warps: the listed classes are written by
-// one warp (another one each row) after the others have passed their stores,
-// without their waiting for it.
-__host__ __device__ constexpr int ring_vecs(int nt) { return nt == 512 ? 4 : 2; }  // per thread and chunk
-__host__ __device__ constexpr int chunk_bytes(int nt) { return nt * 16 * ring_vecs(nt); }
+// and one barrier per row holds the reducing warps: a third warp writes the
+// listed classes and the loss once all have passed their stores, without their
+// waiting for it (done by one of them, it held the others up at the next row's
+// barrier: 268 us on 8192 x 32000 bf16).
+constexpr int kRingVecs = 4;  // vectors per thread and chunk
+__host__ __device__ constexpr int chunk_bytes(int nt) { return nt * 16 * kRingVecs; }
 constexpr int kMaxSlots = 16;
-constexpr int kRingWarps = 2;  // the copying warp and the list warp
+constexpr int kRingWarps = 3;  // copies, lists, listed classes
 
 // Classes of a list with their places added up, by one warp: cls[k] the class
 // of place k and prob[k] its probability with those of its later places, or
@@ -439,13 +443,14 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
     distill_ring_kernel(DistillParams p, RingShape rs) {
     using E = Elem<T>;
     constexpr int ES = E::kBytes;
-    constexpr int V = ring_vecs(NT);
+    constexpr int V = kRingVecs;
     constexpr int CH = chunk_bytes(NT);
     constexpr int VC = CH / 16;
     constexpr int NW = NT / 32;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
-    __shared__ uint64_t list_full[2], list_empty[2];
+    __shared__ uint64_t list_full[2], list_empty[2], row_done[2];
+    __shared__ MS joined[2];
     __shared__ MS part[2][NW];
     __shared__ int fine[2][NW];  // the warp's waits have all been met
     __shared__ float masses[2], negent[2];
@@ -472,6 +477,7 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&list_full[i], 1);
             mbar_init(&list_empty[i], 1);
+            mbar_init(&row_done[i], NW);
         }
         dead = 0;
         fence_mbar_init();
@@ -547,11 +553,56 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
             lb ^= 1;
             if (lb == 0) ph ^= 1u;
         }
+    } else if (warp == NW + 2) {
+        // ---- the listed classes, over the rows' stores, and the losses
+        const float scalar = scalar_grad_scale(p);
+        uint32_t ph = 0;
+        int buf = 0;
+        for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&row_done[buf], ph))) {
+                if (lane == 0) fail();
+                break;
+            }
+            const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
+            const int *cls = cls_of(buf);
+            const float *prob = prob_of(buf);
+            const MS a = joined[buf];
+            const float mass = masses[buf];
+            const float f = row_grad_factor(p, scalar, b) * p.temperature;
+            const float log2S = log2f(a.s);
+            float cross = 0.f;
+#pragma unroll 4
+            for (int k = lane; k < words; k += 32) {
+                const int c = cls[k];
+                const float z = c >= 0 ? E::load_global(row + (size_t)c * ES) : 0.f;
+                if (c < 0) continue;
+                const float lp2 = (z - a.m) * scale - log2S;
+                const float q = prob[k];
+                if (q != 0.f) cross += q * lp2;
+                if (grads)
+                    E::store(p.grad + (size_t)(b * p.C + c) * ES,
+                             mass == 0.f ? 0.f : (mass * ex2(lp2) - q) * f);
+            }
+            cross = warp_sum(cross);
+            if (lane == 0) {
+                float l = (negent[buf] - kLn2 * cross) * p.temperature * p.temperature;
+                if (mass == 0.f) l = 0.f;
+                if (bads[buf]) {
+                    l = NAN;
+                    atomicAdd(&p.err[kErrBadTarget], 1);
+                }
+                p.loss_rows[b] = l;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&list_empty[buf]);
+            buf ^= 1;
+            if (buf == 0) ph ^= 1u;
+        }
     } else {
         // ---- the rows
         const int t = threadIdx.x;
         const float scalar = scalar_grad_scale(p);
-        int s = 0, buf = 0, turn = 0;
+        int s = 0, buf = 0;
         uint32_t ph = 0, lph = 0;
         // A wait that gave up ends the warp's part in this row; the CTA stops
         // at its next barrier, where all warps see the same flags.
@@ -566,25 +617,36 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
             const long long lc = loose(sp, p.C, t);
             const float lz = lc >= 0 ? E::load_global(row + lc * ES) : -INFINITY;
             MS a = {lz, lz == -INFINITY ? 0.f : lz == lz ? 1.f : lz};
-            auto fetch = [&](int slot, long long v, uint4 (&x)[V]) {
+            const int nvec = (int)sp.v1;
+            // chunk at vector v (all of it there, or the row's last) to registers
+            auto fetch = [&](int slot, int v, uint4 (&x)[V]) {
+                const unsigned char *src = ring + slot * CH + t * 16;
+                if (v + VC <= nvec) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int i = k * NT + t;
-                    x[k] = v + i < sp.v1 ? lds128(ring + (size_t)slot * CH + i * 16)
-                                         : make_uint4(E::kNegInfWord, E::kNegInfWord,
-                                                      E::kNegInfWord, E::kNegInfWord);
+                    for (int k = 0; k < V; ++k) x[k] = lds128(src + k * NT * 16);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        x[k] = v + k * NT + t < nvec
+                                   ? lds128(src + k * NT * 16)
+                                   : make_uint4(E::kNegInfWord, E::kNegInfWord, E::kNegInfWord,
+                                                E::kNegInfWord);
                 }
             };
             auto release = [&](int slot) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[slot]);
             };
+            auto release_row = [&](int i) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&row_done[i]);
+            };
             const int s0 = s;
-            for (long long v = 0; v < sp.v1; v += VC) {
+            for (int v = 0; v < nvec; v += VC) {
                 if (wait(&full[s], ph)) {
                     uint4 x[V];
                     fetch(s, v, x);
-                    a = join(a, of_vectors<E, V>(x, scale), scale);
+                    add_vectors<E, V>(a, x, scale);
                     if (!RESIDENT || !grads) release(s);
                 }
                 if (++s == S) {
@@ -611,8 +673,6 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
             const float inv = 1.f / a.s;
             const float mass = masses[buf];
             const float f = row_grad_factor(p, scalar, b) * p.temperature;
-            const bool mine = warp == turn;
-            if (++turn == NW) turn = 0;
             if (grads) {
                 unsigned char *grow = p.grad + (size_t)(b * p.C) * ES;
                 unsigned char *gv = grow + sp.nh * ES;
@@ -620,20 +680,30 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 const float fs = zero ? 0.f : mass * inv * f;
                 if (lc >= 0) E::store(grow + lc * ES, zero ? 0.f : ex2((lz - m) * scale) * fs);
                 int r = RESIDENT ? s0 : s;
-                for (long long v = 0; v < sp.v1; v += VC) {
+                unsigned char *gt = gv + t * 16;
+                for (int v = 0; v < nvec; v += VC, gt += CH) {
                     if (!RESIDENT) wait(&full[r], ph);
                     if (ok) {
                         uint4 x[V];
                         fetch(r, v, x);
                         release(r);
+                        if (zero) {
 #pragma unroll
-                        for (int k = 0; k < V; ++k) {
-                            const long long i = v + k * NT + t;
-                            if (i < sp.v1)
-                                put_vector<E>(gv + i * 16,
-                                              zero ? make_uint4(0u, 0u, 0u, 0u)
-                                                   : gradient_of<E>(x[k], m, scale, fs),
-                                              p.grad_vec_ok);
+                            for (int k = 0; k < V; ++k) x[k] = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < V; ++k)
+                                x[k] = gradient_of<E>(x[k], m, scale, fs);
+                        }
+                        if (v + VC <= nvec && p.grad_vec_ok) {
+#pragma unroll
+                            for (int k = 0; k < V; ++k)
+                                __stcs(reinterpret_cast<uint4 *>(gt + k * NT * 16), x[k]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < V; ++k)
+                                if (v + k * NT + t < nvec)
+                                    put_vector<E>(gt + k * NT * 16, x[k], p.grad_vec_ok);
                         }
                     }
                     if (++r == S) {
@@ -643,40 +713,9 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 }
                 if (!RESIDENT) s = r;
                 if (!ok && lane == 0) fail();
-                // the listed classes go over these stores
-                if (mine)
-                    named_sync(2, NT);
-                else
-                    named_arrive(2, NT);
             }
-            if (mine) {
-                const int *cls = cls_of(buf);
-                const float *prob = prob_of(buf);
-                const float log2S = log2f(a.s);
-                float cross = 0.f;
-                for (int k = lane; k < words; k += 32) {
-                    const int c = cls[k];
-                    if (c < 0) continue;
-                    const float lp2 = (E::load_global(row + (size_t)c * ES) - m) * scale - log2S;
-                    const float q = prob[k];
-                    if (q != 0.f) cross += q * lp2;
-                    if (grads)
-                        E::store(p.grad + (size_t)(b * p.C + c) * ES,
-                                 mass == 0.f ? 0.f : (mass * ex2(lp2) - q) * f);
-                }
-                cross = warp_sum(cross);
-                if (lane == 0) {
-                    float l = (negent[buf] - kLn2 * cross) * p.temperature * p.temperature;
-                    if (mass == 0.f) l = 0.f;
-                    if (bads[buf]) {
-                        l = NAN;
-                        atomicAdd(&p.err[kErrBadTarget], 1);
-                    }
-                    p.loss_rows[b] = l;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&list_empty[buf]);
-            }
+            if (threadIdx.x == 0) joined[buf] = a;
+            release_row(buf);
             buf ^= 1;
             if (buf == 0) lph ^= 1u;
         }
