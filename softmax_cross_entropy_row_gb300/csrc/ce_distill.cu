@@ -13,6 +13,7 @@
 // of exponentials; the group joins them in a fixed order.  Rows that fit the
 // group's registers stay there; longer ones are read a second time, from L2.
 #include <math.h>
+#include <stdlib.h>
 
 #include <map>
 #include <mutex>
@@ -53,10 +54,10 @@ __device__ __forceinline__ MS join(MS a, MS b, float scale) {
 }
 
 // The teacher's list of row b, by one warp: classes and log-probabilities to
-// shared memory (unused and bad places: class -1), the mass to *mass, and
-// whether a class was out of range.
-__device__ __forceinline__ void read_list(const DistillParams &p, long long b, int *idx, float *lq,
-                                          float *mass, int *bad) {
+// shared memory (unused and bad places: class -1), and whether a class was out
+// of range.  Returns the mass.
+__device__ __forceinline__ float read_list(const DistillParams &p, long long b, int *idx,
+                                           float *lq, int *bad) {
     const int lane = threadIdx.x & 31;
     const long long i0 = b * p.K;
     const float inv_t = 1.f / p.temperature;
@@ -94,11 +95,9 @@ __device__ __forceinline__ void read_list(const DistillParams &p, long long b, i
         q += expf(v);
     }
     q = warp_sum(q);
-    wrong = __any_sync(0xffffffffu, wrong);
-    if (lane == 0) {
-        *mass = q;
-        *bad = wrong;
-    }
+    *bad = __any_sync(0xffffffffu, wrong);
+    __syncwarp();
+    return q;
 }
 
 // A row's place in memory: nh elements up to a 16-byte boundary, nvec whole
@@ -129,6 +128,29 @@ __device__ __forceinline__ long long loose(const Span &s, long long C, int t) {
     return c >= s.e0 && c < s.e1 ? c : -1;
 }
 
+// The exponent (z - m) scale of a pair.  m scale is rounded to the multiple of
+// 2^-24 |m scale| that is its fp32 value, so up to 2^6 (an error of 2^-18, of
+// 3e-6 in the exponential) one fused operation does; beyond that (or where
+// the product overflows: rows of the type's lowest values) the difference is
+// formed first, which is exact where it matters.
+struct Exponent {
+    unsigned long long nm, sc, nM;
+    bool small;
+    __device__ __forceinline__ Exponent(float m, float scale) {
+        const float M = m * scale;
+        nm = f2_pack(-m, -m);
+        sc = f2_pack(scale, scale);
+        nM = f2_pack(-M, -M);
+        small = fabsf(M) <= 64.f;
+    }
+    __device__ __forceinline__ unsigned long long fused(unsigned long long z) const {
+        return f2_fma(z, sc, nM);
+    }
+    __device__ __forceinline__ unsigned long long exact(unsigned long long z) const {
+        return f2_mul(f2_add(z, nm), sc);
+    }
+};
+
 // V vectors added to a running maximum and sum, which is rescaled when the
 // maximum grows (after a row's first vectors it hardly ever does).
 template <typename E, int V>
@@ -142,38 +164,52 @@ __device__ __forceinline__ void add_vectors(MS &a, const uint4 (&x)[V], float sc
         a.m = m;
     }
     const float base = a.m == -INFINITY ? 0.f : a.m;
-    const unsigned long long nm2 = f2_pack(-base, -base), sc2 = f2_pack(scale, scale);
+    const Exponent ex(base, scale);
     unsigned long long sum[2] = {0ull, 0ull};
+    auto all = [&](auto exponent) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        unsigned long long z[E::kVec / 2];
-        E::unpack2(x[k], z);
+        for (int k = 0; k < V; ++k) {
+            unsigned long long z[E::kVec / 2];
+            E::unpack2(x[k], z);
 #pragma unroll
-        for (int j = 0; j < E::kVec / 2; ++j) {
-            float u, v;
-            f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), u, v);
-            sum[j & 1] = f2_add(sum[j & 1], f2_pack(ex2(u), ex2(v)));
+            for (int j = 0; j < E::kVec / 2; ++j) {
+                float u, v;
+                f2_unpack(exponent(z[j]), u, v);
+                sum[j & 1] = f2_add(sum[j & 1], f2_pack(ex2(u), ex2(v)));
+            }
         }
-    }
+    };
+    if (ex.small)
+        all([&](unsigned long long z) { return ex.fused(z); });
+    else
+        all([&](unsigned long long z) { return ex.exact(z); });
     float u, v;
     f2_unpack(f2_add(sum[0], sum[1]), u, v);
     a.s += u + v;
 }
 
-// The gradient of a vector: 2^((z - m) scale) f.
-template <typename E>
-__device__ __forceinline__ uint4 gradient_of(const uint4 &x, float m, float scale, float f) {
-    unsigned long long z[E::kVec / 2];
-    const unsigned long long nm2 = f2_pack(-m, -m), sc2 = f2_pack(scale, scale),
-                             f2 = f2_pack(f, f);
-    E::unpack2(x, z);
+// Vectors turned into their gradients, 2^((z - m) scale) f.
+template <typename E, int V>
+__device__ __forceinline__ void to_gradients(uint4 (&x)[V], const Exponent &ex, float f) {
+    const unsigned long long f2 = f2_pack(f, f);
+    auto all = [&](auto exponent) {
 #pragma unroll
-    for (int j = 0; j < E::kVec / 2; ++j) {
-        float a, b;
-        f2_unpack(f2_mul(f2_add(z[j], nm2), sc2), a, b);
-        z[j] = f2_mul(f2_pack(ex2(a), ex2(b)), f2);
-    }
-    return E::pack2(z);
+        for (int k = 0; k < V; ++k) {
+            unsigned long long z[E::kVec / 2];
+            E::unpack2(x[k], z);
+#pragma unroll
+            for (int j = 0; j < E::kVec / 2; ++j) {
+                float u, v;
+                f2_unpack(exponent(z[j]), u, v);
+                z[j] = f2_mul(f2_pack(ex2(u), ex2(v)), f2);
+            }
+            x[k] = E::pack2(z);
+        }
+    };
+    if (ex.small)
+        all([&](unsigned long long z) { return ex.fused(z); });
+    else
+        all([&](unsigned long long z) { return ex.exact(z); });
 }
 
 template <typename E>
@@ -243,7 +279,14 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
 
         int *idx = reinterpret_cast<int *>(lists) + (buf * GROUPS + group) * 2 * p.list_words;
         float *lq = reinterpret_cast<float *>(idx + p.list_words);
-        if (warp == 0) read_list(p, b, idx, lq, &masses[buf][group], &bads[buf][group]);
+        if (warp == 0) {
+            int bad;
+            const float q = read_list(p, b, idx, lq, &bad);
+            if (lane == 0) {
+                masses[buf][group] = q;
+                bads[buf][group] = bad;
+            }
+        }
 
         // this thread's maximum and sum
         MS a = {lz, lz == -INFINITY ? 0.f : lz == lz ? 1.f : lz};
@@ -262,9 +305,9 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
         if constexpr (G > 32) {
             if (lane == 0) part[buf][warp] = a;
             __syncthreads();
-            a = part[buf][0];
-#pragma unroll
-            for (int i = 1; i < WARPS; ++i) a = join(a, part[buf][i], scale);
+            const MS w = lane < WARPS ? part[buf][lane] : MS{-INFINITY, 0.f};
+            a.m = warp_max(w.m);
+            a.s = warp_sum(w.m == -INFINITY ? w.s : w.s * ex2((w.m - a.m) * scale));
             if (cluster > 1) {
                 if (threadIdx.x == 0) mine[buf] = make_float4(a.m, a.s, 0.f, 0.f);
                 cluster_sync();
@@ -288,15 +331,18 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             const bool zero = mass == 0.f;  // no list: nothing to learn, whatever the row holds
             const float fs = zero ? 0.f : mass * inv * f;
             if (lc >= 0) E::store(grow + lc * ES, zero ? 0.f : ex2((lz - m) * scale) * fs);
+            const Exponent ex(m, scale);
             auto write = [&](long long v) {
+                if (zero) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) x[k] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    to_gradients<E, V>(x, ex, fs);
+                }
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const long long i = v + k * G + t;
-                    if (i < sp.v1)
-                        put_vector<E>(gv + i * 16,
-                                      zero ? make_uint4(0u, 0u, 0u, 0u)
-                                           : gradient_of<E>(x[k], m, scale, fs),
-                                      p.grad_vec_ok);
+                    if (i < sp.v1) put_vector<E>(gv + i * 16, x[k], p.grad_vec_ok);
                 }
             };
             if constexpr (LOOP) {
@@ -365,65 +411,100 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
 // ------------------------------------------------------------------- ring
 //
 // Many long rows: a CTA takes one row at a time, streamed through a ring of
-// shared-memory chunks by a warp of its own (TMA bulk copies), while another
-// warp reads the teacher's lists a row ahead.  RESIDENT: the ring holds a row,
-// whose chunks stay for the gradient; otherwise the row is streamed a second
-// time, from L2.  The next row's copies are under way while a row is reduced,
-// and one barrier per row holds the reducing warps: a third warp writes the
-// listed classes and the loss once all have passed their stores, without their
-// waiting for it (done by one of them, it held the others up at the next row's
-// barrier: 268 us on 8192 x 32000 bf16).
-constexpr int kRingVecs = 4;  // vectors per thread and chunk
-__host__ __device__ constexpr int chunk_bytes(int nt) { return nt * 16 * kRingVecs; }
+// shared-memory chunks by a warp of its own (TMA bulk copies).  RESIDENT: the
+// ring holds a row, whose chunks stay for the gradient; otherwise the row is
+// streamed a second time, from L2.  The next row's copies are under way while
+// a row is reduced, and one barrier per row holds the reducing warps.  The
+// teacher's lists belong to warps of their own, which take the rows in turn:
+// one reads its row's list ahead, waits until the others have passed the row's
+// stores, and writes the listed classes and the loss, without their waiting
+// for it (done by one of the reducing warps, it held the others up at the next
+// row's barrier: 268 us on 8192 x 32000 bf16).
+// Vectors per thread and chunk: chunks of 8, 16, 16 and 32 KB.
+__host__ __device__ constexpr int ring_vecs(int nt, bool resident) {
+    return nt == 512 && resident ? 2 : 4;
+}
+__host__ __device__ constexpr int chunk_bytes(int nt, bool resident) {
+    return nt * 16 * ring_vecs(nt, resident);
+}
 constexpr int kMaxSlots = 16;
-constexpr int kRingWarps = 3;  // copies, lists, listed classes
 
-// Classes of a list with their places added up, by one warp: cls[k] the class
-// of place k and prob[k] its probability with those of its later places, or
-// cls[k] = -1 (unused, or an earlier place has the class).  Returns
-// sum_k q_k log q_k.  A hash table (`table`, 2^bits >= 2 words) finds out
-// whether any class is listed twice; the sums run in the list's order.
-__device__ __forceinline__ float merge_list(const int *idx, const float *lq, int words, int *cls,
-                                            float *prob, int *table, int bits) {
+// What a list warp keeps of one row's list, in shared memory.
+struct List {
+    int *cls;        // classes; -1: unused, or an earlier place has the class
+    float *prob;     // probabilities, with those of the class's later places
+    float *z;        // the student's logits there
+    unsigned long long *acc;  // (scratch; z lies in it)
+    int *key, *first;         // hash table of 2^bits >= 2 words places
+};
+__host__ __device__ constexpr int list_bytes(int words, int bits) {
+    return words * 16 + (8 << bits);
+}
+__device__ __forceinline__ List list_at(unsigned char *base, int words, int bits) {
+    List l;
+    l.acc = reinterpret_cast<unsigned long long *>(base);
+    l.z = reinterpret_cast<float *>(base);
+    l.cls = reinterpret_cast<int *>(base + 8 * words);
+    l.prob = reinterpret_cast<float *>(l.cls + words);
+    l.key = reinterpret_cast<int *>(l.prob + words);
+    l.first = l.key + (1 << bits);
+    return l;
+}
+__device__ __forceinline__ int find(const int *key, int bits, int c) {
+    unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
+    for (int n = 0; n < (1 << bits) && key[at] != c; ++n) at = (at + 1) & ((1 << bits) - 1);
+    return (int)at;
+}
+
+// cls and prob (log-probabilities on entry) with the places of a class added
+// up, by one warp; returns sum_k q_k log q_k.  A hash table finds out whether
+// any class is listed twice.  Only then the later places' probabilities are
+// added to the first's, as multiples of 2^-40, whose sums do not depend on the
+// order of the additions.
+__device__ __forceinline__ float merge_list(const List &l, int words, int bits) {
     const int lane = threadIdx.x & 31;
     const int size = 1 << bits;
-    for (int i = lane; i < size; i += 32) table[i] = -1;
+    for (int i = lane; i < size; i += 32) l.key[i] = -1;
     __syncwarp();
     bool twice = false;
     float h = 0.f;
     for (int k = lane; k < words; k += 32) {
-        const int c = idx[k];
+        const int c = l.cls[k];
         float q = 0.f;
         if (c >= 0) {
-            const float v = lq[k];
+            const float v = l.prob[k];
             q = expf(v);
             if (q != 0.f) h += q * v;
             unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
             for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
-                const int was = atomicCAS(&table[at], -1, c);
+                const int was = atomicCAS(&l.key[at], -1, c);
                 twice |= was == c;
                 if (was == -1 || was == c) break;
                 at = (at + 1) & (size - 1);
             }
         }
-        cls[k] = c;
-        prob[k] = q;
+        l.prob[k] = q;
     }
     if (__any_sync(0xffffffffu, twice)) {
+        constexpr float kUnit = 1099511627776.f;  // 2^40
+        for (int i = lane; i < size; i += 32) l.first[i] = words;
+        for (int k = lane; k < words; k += 32) l.acc[k] = 0ull;
+        __syncwarp();
+        for (int k = lane; k < words; k += 32)
+            if (l.cls[k] >= 0) atomicMin(&l.first[find(l.key, bits, l.cls[k])], k);
         __syncwarp();
         for (int k = lane; k < words; k += 32) {
-            const int c = idx[k];
-            if (c < 0) continue;
-            float q = 0.f;
-            bool first = true;
-            for (int j = 0; j < words; ++j) {
-                if (idx[j] != c) continue;
-                if (j < k) first = false;
-                q += expf(lq[j]);
-            }
-            cls[k] = first ? c : -1;
-            prob[k] = q;
+            if (l.cls[k] < 0) continue;
+            const int f = l.first[find(l.key, bits, l.cls[k])];
+            if (f == k) continue;
+            const float q = l.prob[k];
+            atomicAdd(&l.acc[f], (unsigned long long)(fminf(q, 1048576.f) * kUnit));
+            l.cls[k] = -1;
         }
+        __syncwarp();
+        for (int k = lane; k < words; k += 32)
+            l.prob[k] += (float)((double)l.acc[k] * (1.0 / (double)kUnit));
+        __syncwarp();
     }
     return warp_sum(h);
 }
@@ -433,28 +514,28 @@ struct RingShape {
     int table_bits;
 };
 
-// Shared memory of the lists: idx, lq (being read), two of (cls, prob), table.
-__host__ __device__ constexpr int list_bytes(int words, int bits) {
-    return words * 4 * 6 + (4 << bits);
-}
+// List warps of a CTA, each with a list of its own: a row's list is read, and
+// its listed classes are written, while LW - 1 other rows go through the ring,
+// so the latencies of both are hidden.
+__host__ __device__ constexpr int list_warps(int nt) { return nt == 512 ? 4 : 2; }
 
 template <typename T, int NT, bool RESIDENT>
-__global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
+__global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
     distill_ring_kernel(DistillParams p, RingShape rs) {
     using E = Elem<T>;
     constexpr int ES = E::kBytes;
-    constexpr int V = kRingVecs;
-    constexpr int CH = chunk_bytes(NT);
+    constexpr int V = ring_vecs(NT, RESIDENT);
+    constexpr int CH = chunk_bytes(NT, RESIDENT);
     constexpr int VC = CH / 16;
     constexpr int NW = NT / 32;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
-    __shared__ uint64_t list_full[2], list_empty[2], row_done[2];
-    __shared__ MS joined[2];
+    constexpr int LW = list_warps(NT);
+    __shared__ uint64_t list_full[LW], row_done[LW];
+    __shared__ MS joined[LW];
+    __shared__ float masses[LW];
     __shared__ MS part[2][NW];
     __shared__ int fine[2][NW];  // the warp's waits have all been met
-    __shared__ float masses[2], negent[2];
-    __shared__ int bads[2];
     __shared__ int dead;  // a wait gave up
     __shared__ int tail_flag;
     __shared__ float2 tail_scratch[kTailWarps];
@@ -463,20 +544,13 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
     const int lane = threadIdx.x & 31;
     const int S = rs.slots;
     const int words = p.list_words;
-    int *idx = reinterpret_cast<int *>(ring + (size_t)S * CH);
-    float *lq = reinterpret_cast<float *>(idx + words);
-    int *table = idx + 6 * words;
-    auto cls_of = [&](int b) { return idx + 2 * words + b * 2 * words; };
-    auto prob_of = [&](int b) { return reinterpret_cast<float *>(idx + 3 * words + b * 2 * words); };
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], NW);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < LW; ++i) {
             mbar_init(&list_full[i], 1);
-            mbar_init(&list_empty[i], 1);
             mbar_init(&row_done[i], NW);
         }
         dead = 0;
@@ -535,49 +609,39 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 }
             }
         }
-    } else if (warp == NW + 1) {
-        // ---- the lists
-        uint32_t ph = 0;
-        int lb = 0;
-        for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&list_empty[lb], ph ^ 1u))) {
-                if (lane == 0) fail();
-                break;
-            }
-            read_list(p, b, idx, lq, &masses[lb], &bads[lb]);
-            __syncwarp();
-            const float h = merge_list(idx, lq, words, cls_of(lb), prob_of(lb), table, rs.table_bits);
-            if (lane == 0) negent[lb] = h;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&list_full[lb]);
-            lb ^= 1;
-            if (lb == 0) ph ^= 1u;
-        }
-    } else if (warp == NW + 2) {
-        // ---- the listed classes, over the rows' stores, and the losses
+    } else if (warp > NW) {
+        // ---- the lists: this warp's are every LW-th of the CTA's rows
+        const int j = warp - NW - 1;
+        const List l = list_at(ring + (size_t)S * CH + j * list_bytes(words, rs.table_bits), words,
+                               rs.table_bits);
         const float scalar = scalar_grad_scale(p);
         uint32_t ph = 0;
-        int buf = 0;
-        for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&row_done[buf], ph))) {
+        for (long long b = blockIdx.x + (long long)j * gridDim.x; b < p.B;
+             b += (long long)LW * gridDim.x, ph ^= 1u) {
+            const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
+            int bad;
+            const float mass = read_list(p, b, l.cls, l.prob, &bad);
+            if (lane == 0) {
+                masses[j] = mass;
+                mbar_arrive(&list_full[j]);  // the reducing warps need the mass alone
+            }
+            const float negent = merge_list(l, words, rs.table_bits);
+#pragma unroll 4
+            for (int k = lane; k < words; k += 32)
+                l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
+            if (!__all_sync(0xffffffffu, mbar_wait(&row_done[j], ph))) {
                 if (lane == 0) fail();
                 break;
             }
-            const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
-            const int *cls = cls_of(buf);
-            const float *prob = prob_of(buf);
-            const MS a = joined[buf];
-            const float mass = masses[buf];
+            const MS a = joined[j];
             const float f = row_grad_factor(p, scalar, b) * p.temperature;
             const float log2S = log2f(a.s);
             float cross = 0.f;
-#pragma unroll 4
             for (int k = lane; k < words; k += 32) {
-                const int c = cls[k];
-                const float z = c >= 0 ? E::load_global(row + (size_t)c * ES) : 0.f;
+                const int c = l.cls[k];
                 if (c < 0) continue;
-                const float lp2 = (z - a.m) * scale - log2S;
-                const float q = prob[k];
+                const float lp2 = (l.z[k] - a.m) * scale - log2S;
+                const float q = l.prob[k];
                 if (q != 0.f) cross += q * lp2;
                 if (grads)
                     E::store(p.grad + (size_t)(b * p.C + c) * ES,
@@ -585,24 +649,21 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
             }
             cross = warp_sum(cross);
             if (lane == 0) {
-                float l = (negent[buf] - kLn2 * cross) * p.temperature * p.temperature;
-                if (mass == 0.f) l = 0.f;
-                if (bads[buf]) {
-                    l = NAN;
+                float loss = (negent - kLn2 * cross) * p.temperature * p.temperature;
+                if (mass == 0.f) loss = 0.f;
+                if (bad) {
+                    loss = NAN;
                     atomicAdd(&p.err[kErrBadTarget], 1);
                 }
-                p.loss_rows[b] = l;
+                p.loss_rows[b] = loss;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&list_empty[buf]);
-            buf ^= 1;
-            if (buf == 0) ph ^= 1u;
         }
     } else {
         // ---- the rows
         const int t = threadIdx.x;
         const float scalar = scalar_grad_scale(p);
-        int s = 0, buf = 0;
+        int s = 0, buf = 0, lb = 0;
         uint32_t ph = 0, lph = 0;
         // A wait that gave up ends the warp's part in this row; the CTA stops
         // at its next barrier, where all warps see the same flags.
@@ -646,15 +707,15 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 if (wait(&full[s], ph)) {
                     uint4 x[V];
                     fetch(s, v, x);
-                    add_vectors<E, V>(a, x, scale);
                     if (!RESIDENT || !grads) release(s);
+                    add_vectors<E, V>(a, x, scale);
                 }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            if (!wait(&list_full[buf], lph) && lane == 0) fail();
+            if (!wait(&list_full[lb], lph) && lane == 0) fail();
             const float wm = warp_max(a.m);
             a.s = warp_sum(wm == -INFINITY ? a.s : a.s * ex2((a.m - wm) * scale));
             if (lane == 0) {
@@ -662,16 +723,13 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 fine[buf][warp] = ok;
             }
             named_sync(1, NT);
-            bool all = true;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) all = all && fine[buf][i];
-            if (!all) break;
-            a = part[buf][0];
-#pragma unroll
-            for (int i = 1; i < NW; ++i) a = join(a, part[buf][i], scale);
+            const MS w = lane < NW ? part[buf][lane] : MS{-INFINITY, 0.f};
+            if (!__all_sync(0xffffffffu, lane >= NW || fine[buf][lane])) break;
+            a.m = warp_max(w.m);
+            a.s = warp_sum(w.m == -INFINITY ? w.s : w.s * ex2((w.m - a.m) * scale));
             const float m = a.m;
             const float inv = 1.f / a.s;
-            const float mass = masses[buf];
+            const float mass = masses[lb];
             const float f = row_grad_factor(p, scalar, b) * p.temperature;
             if (grads) {
                 unsigned char *grow = p.grad + (size_t)(b * p.C) * ES;
@@ -681,6 +739,7 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 if (lc >= 0) E::store(grow + lc * ES, zero ? 0.f : ex2((lz - m) * scale) * fs);
                 int r = RESIDENT ? s0 : s;
                 unsigned char *gt = gv + t * 16;
+                const Exponent ex(m, scale);
                 for (int v = 0; v < nvec; v += VC, gt += CH) {
                     if (!RESIDENT) wait(&full[r], ph);
                     if (ok) {
@@ -691,9 +750,7 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
 #pragma unroll
                             for (int k = 0; k < V; ++k) x[k] = make_uint4(0u, 0u, 0u, 0u);
                         } else {
-#pragma unroll
-                            for (int k = 0; k < V; ++k)
-                                x[k] = gradient_of<E>(x[k], m, scale, fs);
+                            to_gradients<E, V>(x, ex, fs);
                         }
                         if (v + VC <= nvec && p.grad_vec_ok) {
 #pragma unroll
@@ -714,10 +771,13 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
                 if (!RESIDENT) s = r;
                 if (!ok && lane == 0) fail();
             }
-            if (threadIdx.x == 0) joined[buf] = a;
-            release_row(buf);
+            if (threadIdx.x == 0) joined[lb] = a;
+            release_row(lb);
             buf ^= 1;
-            if (buf == 0) lph ^= 1u;
+            if (++lb == LW) {
+                lb = 0;
+                lph ^= 1u;
+            }
         }
     }
     __syncthreads();
@@ -734,10 +794,14 @@ __global__ void __launch_bounds__(NT + 32 * kRingWarps, NT == 512 ? 1 : 2)
 // two passes.
 template <typename T>
 const void *kernel_of(const DistillPlan &pl) {
+    if (pl.ring_threads && !pl.resident)
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, false>);
+    if (pl.ring_threads == 128)
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 128, true>);
     if (pl.ring_threads == 256)
         return reinterpret_cast<const void *>(distill_ring_kernel<T, 256, true>);
     if (pl.ring_threads == 512)
-        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, false>);
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, true>);
     if (pl.loop) return reinterpret_cast<const void *>(distill_kernel<T, 512, 8, true>);
     if (pl.group == 32 && pl.vecs == 8)
         return reinterpret_cast<const void *>(distill_kernel<T, 32, 8, false>);
@@ -752,7 +816,7 @@ const void *kernel_of(int dtype, const DistillPlan &pl) {
 }
 
 int threads_of(const DistillPlan &pl) {
-    if (pl.ring_threads) return pl.ring_threads + 32 * kRingWarps;
+    if (pl.ring_threads) return pl.ring_threads + 32 + 32 * list_warps(pl.ring_threads);
     return pl.group == 32 ? 256 : pl.group;
 }
 
@@ -780,6 +844,14 @@ cudaError_t resident(const void *f, int threads, int smem, int *n) {
 constexpr int kSmemPerSm = 228 * 1024;
 constexpr int kSmemReserve = 2048;
 
+int fill100() {
+    static const int v = [] {
+        const char *e = getenv("CE_DISTILL_FILL");
+        return e ? atoi(e) : 200;
+    }();
+    return v;
+}
+
 cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
                          DistillPlan *pl) {
     const long long row = C * (dtype == 0 ? 4 : 2);
@@ -802,18 +874,25 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
     }
     const int words = (K + 3) / 4 * 4;
     if (row > 8192 && B > sms) {
-        // the ring: a row resident in the smaller one (two CTAs per SM) if it
-        // takes no more than its bytes, else streamed twice (one CTA per SM)
+        // the ring of the smallest CTA that holds `fill` rows or more (the
+        // next row's copies then run while a row is reduced); rows too long for
+        // that are streamed twice
         r.table_bits = 1;
         while ((1 << r.table_bits) < 2 * words) ++r.table_bits;
-        const int lists = list_bytes(words, r.table_bits);
-        const int two = (kSmemPerSm / 2 - kSmemReserve - lists) / chunk_bytes(256);
-        const bool resident = row <= (long long)two * chunk_bytes(256);
+        int lists = 0;
         r.cluster = 1;
-        r.ring_threads = resident ? 256 : 512;
-        const int room = resident ? two : (kSmemPerSm - kSmemReserve - lists) / chunk_bytes(512);
-        r.slots = room < kMaxSlots ? room : kMaxSlots;
-        r.smem = r.slots * chunk_bytes(r.ring_threads) + lists;
+        for (int nt : {128, 256, 512, 0}) {
+            r.resident = nt != 0;
+            r.ring_threads = nt ? nt : 512;
+            lists = list_warps(r.ring_threads) * list_bytes(words, r.table_bits);
+            const int room = (kSmemPerSm * r.ring_threads / 512 - kSmemReserve - lists) /
+                             chunk_bytes(r.ring_threads, r.resident);
+            r.slots = room < kMaxSlots ? room : kMaxSlots;
+            if (!r.resident || row * fill100() <=
+                                   100LL * r.slots * chunk_bytes(r.ring_threads, true))
+                break;
+        }
+        r.smem = r.slots * chunk_bytes(r.ring_threads, r.resident) + lists;
     }
     const int groups = r.group == 32 ? 8 : 1;
     if (!r.ring_threads) r.smem = 2 * groups * 2 * words * 4;

@@ -25,7 +25,7 @@ struct DistillParams : ParamsEx {
 // `ring_threads` (else 0): rows go through a ring of `slots` chunks instead.
 struct DistillPlan {
     int group, vecs, cluster;
-    bool loop;
+    bool loop, resident;
     int ring_threads, slots, table_bits;
     int ctas;
     int smem;
