@@ -13,7 +13,6 @@
 // of exponentials; the group joins them in a fixed order.  Rows that fit the
 // group's registers stay there; longer ones are read a second time, from L2.
 #include <math.h>
-#include <stdlib.h>
 
 #include <map>
 #include <mutex>
@@ -31,6 +30,13 @@ __device__ __forceinline__ uint4 ld_row(const uint4 *ptr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(ptr));
     return v;
+}
+
+// A warp's prefetch of bytes [p, p + n) to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, long long n) {
+    const char *c = static_cast<const char *>(p);
+    for (long long i = (threadIdx.x & 31) * 128LL; i < n; i += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(c + i));
 }
 
 template <typename V>
@@ -98,6 +104,86 @@ __device__ __forceinline__ float read_list(const DistillParams &p, long long b, 
     *bad = __any_sync(0xffffffffu, wrong);
     __syncwarp();
     return q;
+}
+
+// What one warp keeps of a row's list, in shared memory.
+struct List {
+    int *cls;        // classes; -1: unused, or an earlier place has the class
+    float *prob;     // probabilities, with those of the class's later places
+    float *z;        // the student's logits there
+    unsigned long long *acc;  // (scratch; z lies in it)
+    int *key, *first;         // hash table of 2^bits >= 2 words places
+};
+__host__ __device__ constexpr int list_bytes(int words, int bits) {
+    return words * 16 + (8 << bits);
+}
+__device__ __forceinline__ List list_at(unsigned char *base, int words, int bits) {
+    List l;
+    l.acc = reinterpret_cast<unsigned long long *>(base);
+    l.z = reinterpret_cast<float *>(base);
+    l.cls = reinterpret_cast<int *>(base + 8 * words);
+    l.prob = reinterpret_cast<float *>(l.cls + words);
+    l.key = reinterpret_cast<int *>(l.prob + words);
+    l.first = l.key + (1 << bits);
+    return l;
+}
+__device__ __forceinline__ int find(const int *key, int bits, int c) {
+    unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
+    for (int n = 0; n < (1 << bits) && key[at] != c; ++n) at = (at + 1) & ((1 << bits) - 1);
+    return (int)at;
+}
+
+// cls and prob (log-probabilities on entry) with the places of a class added
+// up, by one warp; returns sum_k q_k log q_k.  A hash table finds out whether
+// any class is listed twice.  Only then the later places' probabilities are
+// added to the first's, as multiples of 2^-40, whose sums do not depend on the
+// order of the additions.
+__device__ __forceinline__ float merge_list(const List &l, int words, int bits) {
+    const int lane = threadIdx.x & 31;
+    const int size = 1 << bits;
+    for (int i = lane; i < size; i += 32) l.key[i] = -1;
+    __syncwarp();
+    bool twice = false;
+    float h = 0.f;
+    for (int k = lane; k < words; k += 32) {
+        const int c = l.cls[k];
+        float q = 0.f;
+        if (c >= 0) {
+            const float v = l.prob[k];
+            q = expf(v);
+            if (q != 0.f) h += q * v;
+            unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
+            for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
+                const int was = atomicCAS(&l.key[at], -1, c);
+                twice |= was == c;
+                if (was == -1 || was == c) break;
+                at = (at + 1) & (size - 1);
+            }
+        }
+        l.prob[k] = q;
+    }
+    if (__any_sync(0xffffffffu, twice)) {
+        constexpr float kUnit = 1099511627776.f;  // 2^40
+        for (int i = lane; i < size; i += 32) l.first[i] = words;
+        for (int k = lane; k < words; k += 32) l.acc[k] = 0ull;
+        __syncwarp();
+        for (int k = lane; k < words; k += 32)
+            if (l.cls[k] >= 0) atomicMin(&l.first[find(l.key, bits, l.cls[k])], k);
+        __syncwarp();
+        for (int k = lane; k < words; k += 32) {
+            if (l.cls[k] < 0) continue;
+            const int f = l.first[find(l.key, bits, l.cls[k])];
+            if (f == k) continue;
+            const float q = l.prob[k];
+            atomicAdd(&l.acc[f], (unsigned long long)(fminf(q, 1048576.f) * kUnit));
+            l.cls[k] = -1;
+        }
+        __syncwarp();
+        for (int k = lane; k < words; k += 32)
+            l.prob[k] += (float)((double)l.acc[k] * (1.0 / (double)kUnit));
+        __syncwarp();
+    }
+    return warp_sum(h);
 }
 
 // A row's place in memory: nh elements up to a 16-byte boundary, nvec whole
@@ -228,7 +314,7 @@ constexpr int min_ctas(int g, int v, bool loop) {
 }
 
 template <typename T, int G, int V, bool LOOP>
-__global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) distill_kernel(DistillParams p, int cluster) {
+__global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) distill_kernel(DistillParams p, int cluster, int bits) {
     using E = Elem<T>;
     constexpr int ES = E::kBytes;
     constexpr int NT = G == 32 ? 256 : G;
@@ -238,8 +324,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
     __shared__ MS part[2][WARPS * GROUPS];
     __shared__ float lpart[2][WARPS * GROUPS];
     __shared__ float4 mine[2];  // this CTA's share, read by the cluster
-    __shared__ float masses[2][GROUPS];
-    __shared__ int bads[2][GROUPS];
+    __shared__ float masses[2];
+    __shared__ int bads[2];
     __shared__ int tail_flag;
     __shared__ float2 tail_scratch[kTailWarps];
 
@@ -277,14 +363,32 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
         const long long lc = loose(sp, p.C, t);
         const float lz = lc >= 0 ? E::load_global(row + lc * ES) : -INFINITY;
 
-        int *idx = reinterpret_cast<int *>(lists) + (buf * GROUPS + group) * 2 * p.list_words;
+        int *idx = reinterpret_cast<int *>(lists) + buf * 2 * p.list_words;
         float *lq = reinterpret_cast<float *>(idx + p.list_words);
-        if (warp == 0) {
+        List l = {};
+        float warp_mass = 0.f, warp_negent = 0.f;
+        int warp_bad = 0;
+        if constexpr (G == 32) {
+            l = list_at(lists + group * list_bytes(p.list_words, bits), p.list_words, bits);
+            // the next row of this warp on its way to L2
+            if (b + step < p.B) {
+                const long long i1 = (b + step) * p.K;
+                const int vs = p.val_dtype == 0 ? 4 : 2;
+                prefetch_l2(row + (size_t)(step * p.C) * ES, p.C * ES);
+                prefetch_l2(p.idx + i1, 4LL * p.K);
+                prefetch_l2(static_cast<const unsigned char *>(p.val) + i1 * vs, (long long)vs * p.K);
+            }
+            warp_mass = read_list(p, b, l.cls, l.prob, &warp_bad);
+            warp_negent = merge_list(l, p.list_words, bits);
+#pragma unroll 2
+            for (int k = lane; k < p.list_words; k += 32)
+                l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
+        } else if (warp == 0) {
             int bad;
             const float q = read_list(p, b, idx, lq, &bad);
             if (lane == 0) {
-                masses[buf][group] = q;
-                bads[buf][group] = bad;
+                masses[buf] = q;
+                bads[buf] = bad;
             }
         }
 
@@ -321,7 +425,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             __syncwarp();
         }
         const float m = a.m, S = a.s;
-        const float mass = masses[buf][group];
+        const float mass = G == 32 ? warp_mass : masses[buf];
         const float f = row_grad_factor(p, scalar, b) * p.temperature;
         const float inv = 1.f / S;
 
@@ -358,7 +462,32 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
 
         // the listed classes, and the loss
         const float log2S = log2f(S);
-        float l = 0.f;
+        if constexpr (G == 32) {
+            float cross = 0.f;
+            for (int k = lane; k < p.list_words; k += 32) {
+                const int c = l.cls[k];
+                if (c < 0) continue;
+                const float lp2 = (l.z[k] - m) * scale - log2S;
+                const float q = l.prob[k];
+                if (q != 0.f) cross += q * lp2;
+                if (writes_grad(p))
+                    E::store(p.grad + (size_t)(b * p.C + c) * ES,
+                             mass == 0.f ? 0.f : (mass * ex2(lp2) - q) * f);
+            }
+            cross = warp_sum(cross);
+            if (lane == 0) {
+                float loss = (warp_negent - kLn2 * cross) * p.temperature * p.temperature;
+                if (mass == 0.f) loss = 0.f;
+                if (warp_bad) {
+                    loss = NAN;
+                    atomicAdd(&p.err[kErrBadTarget], 1);
+                }
+                p.loss_rows[b] = loss;
+            }
+            __syncwarp();
+            continue;
+        }
+        float loss = 0.f;
         for (int k = t; k < p.K; k += G) {
             const int c = idx[k];
             if (c < 0) continue;
@@ -367,7 +496,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             const float lp2 = (E::load_global(row + (size_t)c * ES) - m) * scale - log2S;
             const float v = lq[k];
             const float q = expf(v);
-            if (q != 0.f) l += q * (v - kLn2 * lp2);
+            if (q != 0.f) loss += q * (v - kLn2 * lp2);
             if (!writes_grad(p) || !here) continue;
             float all = 0.f;
             bool mine_first = true;
@@ -386,21 +515,19 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
                          mass == 0.f ? 0.f : (mass * ex2(lp2) - all) * f);
         }
         if (rank == 0) {
-            l = warp_sum(l);
-            if constexpr (G > 32) {
-                if (lane == 0) lpart[buf][warp] = l;
-                __syncthreads();
-                l = lpart[buf][0];
-                for (int i = 1; i < WARPS; ++i) l += lpart[buf][i];
-            }
+            loss = warp_sum(loss);
+            if (lane == 0) lpart[buf][warp] = loss;
+            __syncthreads();
+            loss = lpart[buf][0];
+            for (int i = 1; i < WARPS; ++i) loss += lpart[buf][i];
             if (t == 0) {
-                l *= p.temperature * p.temperature;
-                if (mass == 0.f) l = 0.f;
-                if (bads[buf][group]) {
-                    l = NAN;
+                loss *= p.temperature * p.temperature;
+                if (mass == 0.f) loss = 0.f;
+                if (bads[buf]) {
+                    loss = NAN;
                     atomicAdd(&p.err[kErrBadTarget], 1);
                 }
-                p.loss_rows[b] = l;
+                p.loss_rows[b] = loss;
             }
         }
     }
@@ -429,86 +556,6 @@ __host__ __device__ constexpr int chunk_bytes(int nt, bool resident) {
 }
 constexpr int kMaxSlots = 16;
 
-// What a list warp keeps of one row's list, in shared memory.
-struct List {
-    int *cls;        // classes; -1: unused, or an earlier place has the class
-    float *prob;     // probabilities, with those of the class's later places
-    float *z;        // the student's logits there
-    unsigned long long *acc;  // (scratch; z lies in it)
-    int *key, *first;         // hash table of 2^bits >= 2 words places
-};
-__host__ __device__ constexpr int list_bytes(int words, int bits) {
-    return words * 16 + (8 << bits);
-}
-__device__ __forceinline__ List list_at(unsigned char *base, int words, int bits) {
-    List l;
-    l.acc = reinterpret_cast<unsigned long long *>(base);
-    l.z = reinterpret_cast<float *>(base);
-    l.cls = reinterpret_cast<int *>(base + 8 * words);
-    l.prob = reinterpret_cast<float *>(l.cls + words);
-    l.key = reinterpret_cast<int *>(l.prob + words);
-    l.first = l.key + (1 << bits);
-    return l;
-}
-__device__ __forceinline__ int find(const int *key, int bits, int c) {
-    unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
-    for (int n = 0; n < (1 << bits) && key[at] != c; ++n) at = (at + 1) & ((1 << bits) - 1);
-    return (int)at;
-}
-
-// cls and prob (log-probabilities on entry) with the places of a class added
-// up, by one warp; returns sum_k q_k log q_k.  A hash table finds out whether
-// any class is listed twice.  Only then the later places' probabilities are
-// added to the first's, as multiples of 2^-40, whose sums do not depend on the
-// order of the additions.
-__device__ __forceinline__ float merge_list(const List &l, int words, int bits) {
-    const int lane = threadIdx.x & 31;
-    const int size = 1 << bits;
-    for (int i = lane; i < size; i += 32) l.key[i] = -1;
-    __syncwarp();
-    bool twice = false;
-    float h = 0.f;
-    for (int k = lane; k < words; k += 32) {
-        const int c = l.cls[k];
-        float q = 0.f;
-        if (c >= 0) {
-            const float v = l.prob[k];
-            q = expf(v);
-            if (q != 0.f) h += q * v;
-            unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
-            for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
-                const int was = atomicCAS(&l.key[at], -1, c);
-                twice |= was == c;
-                if (was == -1 || was == c) break;
-                at = (at + 1) & (size - 1);
-            }
-        }
-        l.prob[k] = q;
-    }
-    if (__any_sync(0xffffffffu, twice)) {
-        constexpr float kUnit = 1099511627776.f;  // 2^40
-        for (int i = lane; i < size; i += 32) l.first[i] = words;
-        for (int k = lane; k < words; k += 32) l.acc[k] = 0ull;
-        __syncwarp();
-        for (int k = lane; k < words; k += 32)
-            if (l.cls[k] >= 0) atomicMin(&l.first[find(l.key, bits, l.cls[k])], k);
-        __syncwarp();
-        for (int k = lane; k < words; k += 32) {
-            if (l.cls[k] < 0) continue;
-            const int f = l.first[find(l.key, bits, l.cls[k])];
-            if (f == k) continue;
-            const float q = l.prob[k];
-            atomicAdd(&l.acc[f], (unsigned long long)(fminf(q, 1048576.f) * kUnit));
-            l.cls[k] = -1;
-        }
-        __syncwarp();
-        for (int k = lane; k < words; k += 32)
-            l.prob[k] += (float)((double)l.acc[k] * (1.0 / (double)kUnit));
-        __syncwarp();
-    }
-    return warp_sum(h);
-}
-
 struct RingShape {
     int slots;
     int table_bits;
@@ -517,7 +564,7 @@ struct RingShape {
 // List warps of a CTA, each with a list of its own: a row's list is read, and
 // its listed classes are written, while LW - 1 other rows go through the ring,
 // so the latencies of both are hidden.
-__host__ __device__ constexpr int list_warps(int nt) { return nt == 512 ? 4 : 2; }
+__host__ __device__ constexpr int list_warps(int nt) { return nt == 128 ? 3 : 4; }
 
 template <typename T, int NT, bool RESIDENT>
 __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
@@ -844,21 +891,17 @@ cudaError_t resident(const void *f, int threads, int smem, int *n) {
 constexpr int kSmemPerSm = 228 * 1024;
 constexpr int kSmemReserve = 2048;
 
-int fill100() {
-    static const int v = [] {
-        const char *e = getenv("CE_DISTILL_FILL");
-        return e ? atoi(e) : 200;
-    }();
-    return v;
-}
-
 cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
                          DistillPlan *pl) {
     const long long row = C * (dtype == 0 ? 4 : 2);
     DistillPlan r = {};
     r.cluster = 1;
     r.vecs = 16;
-    if (row <= 8192) {
+    const int words = (K + 3) / 4 * 4;
+    r.table_bits = 1;
+    while ((1 << r.table_bits) < 2 * words) ++r.table_bits;
+    // eight lists per CTA of the warp-per-row kernel: up to 256 places each
+    if (row <= 8192 && 8 * list_bytes(words, r.table_bits) <= 65536) {
         r.group = 32;
         if (row <= 4096) r.vecs = 8;
     } else {
@@ -872,13 +915,14 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
             r.vecs = 8;
         }
     }
-    const int words = (K + 3) / 4 * 4;
-    if (row > 8192 && B > sms) {
-        // the ring of the smallest CTA that holds `fill` rows or more (the
-        // next row's copies then run while a row is reduced); rows too long for
-        // that are streamed twice
-        r.table_bits = 1;
-        while ((1 << r.table_bits) < 2 * words) ++r.table_bits;
+    if (r.group != 32 && B > sms) {
+        // The ring of the smallest CTA that holds the row, of 512 threads only
+        // where it holds 1.7 rows; longer rows are streamed twice.  Measured
+        // (K = 64, bf16 and fp32, fraction of the copy bandwidth): 31 KB rows
+        // 0.77 in 128 threads (0.66-0.73 in 256), 62 KB rows 0.86 in 256 (0.70-
+        // 0.77 in 512), 94 KB fp32 rows 0.90 in 512 threads, 128 KB bf16 rows
+        // 0.98 streamed twice (0.89 resident in 512), 196 KB fp32 rows 0.94
+        // streamed twice (0.91 resident).
         int lists = 0;
         r.cluster = 1;
         for (int nt : {128, 256, 512, 0}) {
@@ -888,14 +932,14 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
             const int room = (kSmemPerSm * r.ring_threads / 512 - kSmemReserve - lists) /
                              chunk_bytes(r.ring_threads, r.resident);
             r.slots = room < kMaxSlots ? room : kMaxSlots;
-            if (!r.resident || row * fill100() <=
-                                   100LL * r.slots * chunk_bytes(r.ring_threads, true))
-                break;
+            const long long held = (long long)r.slots * chunk_bytes(r.ring_threads, true);
+            if (!r.resident || row * (nt == 512 ? 17 : 10) <= held * 10) break;
         }
         r.smem = r.slots * chunk_bytes(r.ring_threads, r.resident) + lists;
     }
     const int groups = r.group == 32 ? 8 : 1;
-    if (!r.ring_threads) r.smem = 2 * groups * 2 * words * 4;
+    if (!r.ring_threads)
+        r.smem = groups == 8 ? 8 * list_bytes(words, r.table_bits) : 2 * 2 * words * 4;
     const void *f = kernel_of(dtype, r);
     cudaError_t e = ensure_smem_attr(f, r.smem);
     if (e != cudaSuccess) return e;
@@ -926,9 +970,10 @@ cudaError_t launch_distill(const DistillParams &p, int dtype, const DistillPlan 
     cfg.attrs = attr;
     cfg.numAttrs = pl.cluster > 1 ? 2 : 1;
     DistillParams q = p;
-    int cluster = pl.cluster;
+    int cluster = pl.cluster, bits = pl.table_bits;
     RingShape ring = {pl.slots, pl.table_bits};
-    void *args[] = {&q, pl.ring_threads ? static_cast<void *>(&ring) : &cluster};
+    void *direct[] = {&q, &cluster, &bits}, *ringed[] = {&q, &ring};
+    void **args = pl.ring_threads ? ringed : direct;
     return cudaLaunchKernelExC(&cfg, kernel_of(dtype, pl), args);
 }
 
