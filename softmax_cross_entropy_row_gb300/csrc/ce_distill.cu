@@ -96,7 +96,8 @@ __device__ __forceinline__ float read_list(const DistillParams &p, long long b, 
     float q = 0.f;
     for (int k = lane; k < p.K; k += 32) {
         if (idx[k] < 0) continue;
-        const float v = (lq[k] - m) * inv_t - ref;
+        // m = -inf: no place has a probability
+        const float v = m == -INFINITY ? -INFINITY : (lq[k] - m) * inv_t - ref;
         lq[k] = v;
         q += expf(v);
     }

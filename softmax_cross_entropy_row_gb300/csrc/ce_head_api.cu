@@ -133,22 +133,22 @@ long long rows_per_piece(long long B, long long D, long long C, bool dweight) {
     return std::min(round_up(B, ce::kTileM), std::max<long long>(r, ce::kTileM));
 }
 
-// Parts of a contraction of kb stages over `tiles` tiles: the number that
-// gives the least time by count of waves, a stage of a tile taking 0.3 us and
-// an fp32 part of a tile 2 x 256 KB at the memory's rate over all SMs.
-int parts_of(long long tiles, long long kb, int pairs) {
-    double best = 1e30;
-    int splits = 1;
-    for (int s = 1; s <= 32 && s <= std::max<long long>(1, kb / 4); ++s) {
-        const double waves = (double)ceil_div(tiles * s, pairs);
-        const double t = waves * (double)ceil_div(kb, s) * 0.3 +
-                         (s > 1 ? 4.0 + (double)tiles * s * 2.0 * 0.262144 / 6.7 : 0.0);
-        if (t < best * 0.97) {
-            best = t;
-            splits = s;
+// Width of the loss alone's column tiles for rows that fill one tile at most
+// (the weights are then read at the memory's rate and the matrix instructions
+// have time): the one that spreads the classes evenly over the pairs.
+int stats_tile(long long C, long long rows, int pairs) {
+    int best = ce::kTileN;
+    if (rows > ce::kTileM) return best;
+    long long least = 1LL << 60;
+    for (int tn = ce::kTileN; tn >= 64; tn -= 32) {
+        const long long rounds = ceil_div(ceil_div(C, tn), pairs);
+        const long long cost = rounds * (tn + 8);
+        if (cost < least) {
+            least = cost;
+            best = tn;
         }
     }
-    return splits;
+    return best;
 }
 
 struct Call {
@@ -217,49 +217,54 @@ int check(const Call &c) {
     return CE_OK;
 }
 
-// Hands out the workspace's parts, 256-byte aligned (first pass: sizes alone).
+// Hands out the workspace's parts, 1 KB aligned (first pass: sizes alone).
 struct Carver {
     unsigned char *base = nullptr;
-    size_t used = 256;  // HeadInfo
+    size_t used = 1024;  // HeadInfo
     template <typename T>
     T *take(size_t n) {
         T *p = reinterpret_cast<T *>(base + used);
-        used += (n * sizeof(T) + 255) / 256 * 256;
+        used += (n * sizeof(T) + 1023) / 1024 * 1024;
         return p;
     }
 };
 
 struct Parts {
     ce::HeadInfo *info;
-    float *loss, *zt, *logq, *zk, *mass, *hidden_parts, *weight_parts;
+    float *loss, *zt, *ref, *logq, *zk, *mass, *parts, *weight;
     float2 *stats;
     ce::HeadRow *row;
-    unsigned char *exps;
+    int *perm, *pos;
+    unsigned char *exps, *packed, *scaled;
 };
 
 struct Sizes {
-    long long piece, pieces, ld, tiles;       // rows per piece, pieces, exponentials' row, tiles
-    int hidden_splits, weight_splits;
-    long long hidden_slab, weight_slab;       // rows of an fp32 part
-    bool weight_f32;
+    long long piece, pieces, ld;  // rows per piece, pieces, exponentials' row
+    int tile_n, tiles;
+    bool grad, per_row, weight_f32;
 };
 
-Parts carve(Carver &w, const Call &c, const Sizes &z) {
-    const bool teacher = c.targets == nullptr, grad = c.dhidden || c.dweight;
+Parts carve(Carver &w, const Call &c, const Sizes &z, int pairs) {
+    const bool teacher = c.targets == nullptr;
+    const size_t padded = round_up(c.B, 64), list = teacher ? (size_t)c.B * c.K : 0;
     Parts p = {};
     p.info = reinterpret_cast<ce::HeadInfo *>(w.base);
     p.loss = w.take<float>(c.reduction == CE_REDUCE_NONE ? 0 : round_up(c.B, 1024));
     p.stats = w.take<float2>((size_t)z.tiles * z.piece);
     p.row = w.take<ce::HeadRow>(z.piece);
-    p.zt = w.take<float>(teacher ? 0 : z.piece);
-    p.logq = w.take<float>(teacher ? (size_t)c.B * c.K : 0);
-    p.zk = w.take<float>(teacher ? (size_t)c.B * c.K : 0);
+    p.zt = w.take<float>(teacher ? 0 : c.B);
+    p.logq = w.take<float>(list);
+    p.zk = w.take<float>(list);
     p.mass = w.take<float>(teacher ? c.B : 0);
-    p.exps = w.take<unsigned char>(grad ? (size_t)z.piece * z.ld * 2 : 0);
-    p.hidden_parts = w.take<float>(c.dhidden && z.hidden_splits > 1
-                                       ? (size_t)z.hidden_splits * z.hidden_slab * c.D : 0);
-    p.weight_parts = w.take<float>(c.dweight && z.weight_f32
-                                       ? (size_t)z.weight_splits * z.weight_slab * c.D : 0);
+    if (!z.grad) return p;
+    p.ref = w.take<float>(c.B);
+    p.perm = w.take<int>(c.B);
+    p.pos = w.take<int>(c.B);
+    p.packed = w.take<unsigned char>(padded * c.D * 2);
+    p.scaled = w.take<unsigned char>(z.per_row && c.dweight ? round_up(z.piece, 64) * c.D * 2 : 0);
+    p.exps = w.take<unsigned char>((size_t)round_up(z.piece, 64) * z.ld * 2);
+    p.parts = w.take<float>((size_t)ce::kMaxParts * pairs * ce::kTileM * ce::kTileN);
+    p.weight = w.take<float>(c.dweight && z.weight_f32 ? (size_t)c.C * c.D : 0);
     return p;
 }
 
@@ -286,44 +291,40 @@ int run(const Call &c) {
     int *err = nullptr;
     CE_TRY(ce::host_error_counters(dev, s, &err));
 
-    const bool teacher = c.targets == nullptr, grad = c.dhidden || c.dweight;
+    const bool teacher = c.targets == nullptr;
     const bool bf16 = c.dtype == CE_BF16, none = c.reduction == CE_REDUCE_NONE;
     const int pairs = sms / 2;
     Sizes z = {};
+    z.grad = c.dhidden || c.dweight;
+    z.per_row = z.grad && bf16;
     z.ld = round_up(c.C, 64);
-    z.tiles = ceil_div(c.C, ce::kTileN);
-    z.piece = grad ? rows_per_piece(c.B, c.D, c.C, c.dweight != nullptr)
-                   : std::min(round_up(c.B, ce::kTileM),
-                              std::max<long long>(ce::kTileM, kPieceBytes / (8 * z.tiles) /
-                                                                  ce::kTileM * ce::kTileM));
+    z.tile_n = z.grad ? ce::kTileN : stats_tile(c.C, c.B, pairs);
+    z.tiles = (int)ceil_div(c.C, z.tile_n);
+    z.piece = z.grad ? rows_per_piece(c.B, c.D, c.C, c.dweight != nullptr)
+                     : std::min(round_up(c.B, ce::kTileM),
+                                std::max<long long>(ce::kTileM, kPieceBytes / (8LL * z.tiles) /
+                                                                    ce::kTileM * ce::kTileM));
     z.pieces = ceil_div(c.B, z.piece);
     z.piece = std::min<long long>(z.piece, c.B);
-    z.hidden_slab = round_up(z.piece, ce::kTileM);
-    z.weight_slab = round_up(c.C, ce::kTileM);
-    z.hidden_splits = parts_of(ceil_div(z.piece, ce::kTileM) * ceil_div(c.D, ce::kTileN),
-                               ceil_div(c.C, ce::kTileK), pairs);
-    z.weight_splits = parts_of(z.tiles * ceil_div(c.D, ce::kTileN),
-                               ceil_div(z.piece, ce::kTileK), pairs);
-    z.weight_f32 = z.pieces > 1 || z.weight_splits > 1;
-    if (z.hidden_slab * z.hidden_splits > 0x7fffffffLL ||
-        z.weight_slab * z.weight_splits > 0x7fffffffLL)
-        return CE_ERR_SHAPE;
+    z.weight_f32 = z.pieces > 1;
 
     std::lock_guard<std::mutex> lk(g_mu);
     Carver sizer;
-    carve(sizer, c, z);
+    carve(sizer, c, z, pairs);
     Carver w;
     CE_TRY(workspace(dev, s, sizer.used, &w.base));
-    const Parts ws = carve(w, c, z);
+    const Parts ws = carve(w, c, z, pairs);
 
-    // f16 holds values down to 2^-24: the kept values (at most 1) are raised
-    // by 2^15 so that small probabilities keep their 11 bits
+    // f16 holds values down to 2^-24: what is kept (at most 1) is raised by
+    // 2^15 so that small probabilities keep their 11 bits
     const float shift = bf16 ? 0.f : 15.f;
     const float shift_mul = bf16 ? 1.f : 32768.f;
     const float *row_scale = none ? c.scale : nullptr;
+    const float exp_scale = ce::kLog2e / (teacher ? c.temperature : 1.f);
+    float *loss_rows = none ? c.loss : ws.loss;
 
-    ce::HeadTeacher t = {};
     if (teacher) {
+        ce::HeadTeacher t = {};
         t.B = c.B;
         t.D = (int)c.D;
         t.C = (int)c.C;
@@ -341,134 +342,181 @@ int run(const Call &c) {
         t.err = err;
         CE_CUDA(ce::launch_head_teacher(t, bf16, sms, s));
     }
-    if (grad || c.reduction == CE_REDUCE_MEAN) {
+    if (z.grad || c.reduction == CE_REDUCE_MEAN) {
         ce::HeadPrep p = {};
         p.B = c.B;
+        p.C = (int)c.C;
         p.targets = c.targets;
         p.ignore_index = c.ignore_index;
-        p.mass = teacher ? ws.mass : nullptr;
+        p.mass = ws.mass;
         p.scale = c.scale;
         p.scale_per_row = row_scale != nullptr;
         p.mean = c.reduction == CE_REDUCE_MEAN;
-        p.alpha = (teacher ? c.temperature : 1.f) / shift_mul;
+        p.mean_of_all = teacher;
+        p.alpha = (teacher ? c.temperature : 1.f) / (z.per_row ? 1.f : shift_mul);
+        p.perm = ws.perm;
+        p.pos = ws.pos;
+        p.loss = loss_rows;
         p.info = ws.info;
+        p.err = err;
         CE_CUDA(ce::launch_head_prep(p, s));
     }
+    if (z.grad) {
+        ce::HeadPack p = {};
+        p.B = c.B;
+        p.C = (int)c.C;
+        p.D = (int)c.D;
+        p.K = (int)c.K;
+        p.pos = ws.pos;
+        p.hidden = static_cast<const unsigned char *>(c.hidden);
+        p.weight = static_cast<const unsigned char *>(c.weight);
+        p.targets = c.targets;
+        p.idx = c.idx;
+        p.zk = ws.zk;
+        p.packed = ws.packed;
+        p.dhidden = static_cast<unsigned char *>(c.dhidden);
+        p.zt = ws.zt;
+        p.ref = z.per_row ? ws.ref : nullptr;
+        p.exp_scale = exp_scale;
+        p.info = ws.info;
+        CE_CUDA(ce::launch_head_pack(p, bf16, s));
+    }
 
-    float *loss_rows = none ? c.loss : ws.loss;
     for (long long i = 0; i < z.pieces; ++i) {
         const long long b0 = i * z.piece;
         const long long rows = std::min<long long>(z.piece, c.B - b0);
+        const long long padded = round_up(rows, 64);
         const unsigned char *h =
             static_cast<const unsigned char *>(c.hidden) + (size_t)b0 * c.D * 2;
+        const unsigned char *hp = ws.packed + (size_t)b0 * c.D * 2;
         ce::HeadGemm g = {};
-        CE_TRY(tensor_map(&g.a, c.dtype, h, rows, c.D, c.D, ce::kTileM / 2));
-        CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileN / 2));
-        if (grad) CE_TRY(tensor_map(&g.out, c.dtype, ws.exps, rows, z.ld, z.ld, 32));
-        g.tiles_m = (int)ceil_div(rows, ce::kTileM);
-        g.tiles_n = (int)z.tiles;
-        g.splits = 1;
-        g.k_blocks = (int)ceil_div(c.D, ce::kTileK);
-        g.group_m = std::min(g.tiles_m, 16);
-        g.exp_scale = ce::kLog2e / (teacher ? c.temperature : 1.f);
-        g.shift = shift;
+        g.info = ws.info;
+        g.B = (int)c.B;
+        g.dynamic = z.grad;
+        g.first = (int)b0;
         g.rows = (int)rows;
-        g.cols = (int)c.C;
-        g.targets = teacher ? nullptr : c.targets + b0;
+        g.C = (int)c.C;
+        g.D = (int)c.D;
+        g.tile_n = z.tile_n;
+        g.alpha = 1.f;
+        g.exp_scale = exp_scale;
+        g.shift = shift;
+        g.targets = c.targets;
+        g.perm = ws.perm;
         g.stats = ws.stats;
-        g.zt = ws.zt;
-        g.write_exp = grad ? 1 : 0;
+        g.zt = teacher ? nullptr : ws.zt + b0;
+        g.ref = z.per_row ? ws.ref + b0 : nullptr;
         g.failed = &ws.info->failed;
-        g.clear_failed = i == 0;
+        g.rescue = &ws.info->rescue;
         g.err = err;
-        CE_CUDA(ce::launch_head_gemm(g, ce::kProdLogits, ce::kEpiLogits, bf16, sms, s));
+        g.parts = ws.parts;
+        g.clear_failed = i == 0;
+        g.clear_rescue = z.per_row;
+        CE_TRY(tensor_map(&g.a, c.dtype, h, rows, c.D, c.D, ce::kTileM / 2));
+        CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, z.tile_n / 2));
+        if (z.grad) {
+            CE_TRY(tensor_map(&g.packed, c.dtype, hp, padded, c.D, c.D, ce::kTileM / 2));
+            CE_TRY(tensor_map(&g.out, c.dtype, ws.exps, padded, z.ld, z.ld, 32));
+        } else {
+            g.packed = g.out = g.a;  // not used
+        }
+        g.group_m = 16;
+        const ce::HeadEpilogue epi =
+            !z.grad ? ce::kEpiStats : z.per_row ? ce::kEpiRef : ce::kEpiKeep;
+        CE_CUDA(ce::launch_head_gemm(g, ce::kProdLogits, epi, bf16, pairs, s));
 
         ce::HeadRows r = {};
-        r.rows = (int)rows;
-        r.cols = (int)c.C;
-        r.tiles = (int)z.tiles;
+        r.B = (int)c.B;
+        r.C = (int)c.C;
+        r.D = (int)c.D;
+        r.dynamic = g.dynamic;
+        r.first = g.first;
+        r.rows = g.rows;
+        r.tiles = z.tiles;
         r.stats = ws.stats;
-        r.zt = ws.zt;
+        r.zt = g.zt;
+        r.ref = z.per_row ? ws.ref + b0 : nullptr;
         r.row = ws.row;
         r.exps = ws.exps;
         r.ld = z.ld;
-        r.exp_scale = g.exp_scale;
+        r.exp_scale = exp_scale;
         r.temperature = c.temperature;
         r.shift_mul = shift_mul;
-        r.targets = g.targets;
+        r.perm = ws.perm;
+        r.targets = c.targets;
         r.ignore_index = c.ignore_index;
-        if (teacher) {
-            r.logq = ws.logq + b0 * c.K;
-            r.idx = c.idx + b0 * c.K;
-            r.zk = ws.zk + b0 * c.K;
-            r.mass = ws.mass + b0;
-            r.K = (int)c.K;
-        }
-        r.row_scale = row_scale ? row_scale + b0 : nullptr;
+        r.logq = ws.logq;
+        r.idx = c.idx;
+        r.zk = ws.zk;
+        r.mass = ws.mass;
+        r.K = (int)c.K;
+        r.row_scale = row_scale;
         r.info = ws.info;
+        r.flag_rescue = 1;
         r.err = err;
-        r.loss = loss_rows + b0;
-        r.want_grad = grad;
-        r.nan_on_failure = none && !grad;
-        CE_CUDA(ce::launch_head_rows(r, s));
-        if (grad) CE_CUDA(ce::launch_head_scale(r, bf16, s));
+        r.loss = loss_rows;
+        r.want_grad = z.grad;
+        r.nan_on_failure = none && !z.grad;
+        r.hidden = h;
+        r.packed = hp;
+        r.scaled = ws.scaled;
+        CE_CUDA(ce::launch_head_rows(r, bf16, s));
+        if (z.per_row) {
+            // again for rows whose reference exponent was too low (both find
+            // nothing to do otherwise)
+            g.clear_failed = g.clear_rescue = 0;
+            g.only_if = r.only_if = &ws.info->rescue;
+            r.flag_rescue = 0;
+            CE_CUDA(ce::launch_head_gemm(g, ce::kProdLogits, epi, bf16, pairs, s));
+            CE_CUDA(ce::launch_head_rows(r, bf16, s));
+            g.only_if = r.only_if = nullptr;
+        } else if (z.grad) {
+            CE_CUDA(ce::launch_head_scale(r, bf16, s));
+        }
         if (teacher) CE_CUDA(ce::launch_head_listed(r, bf16, s));
 
-        g.clear_failed = 0;
-        g.cols = (int)c.D;
-        g.scale = &ws.info->out;
-        g.alpha = 1.f;
+        g.clear_failed = g.clear_rescue = 0;
         if (c.dhidden) {
-            unsigned char *dh = static_cast<unsigned char *>(c.dhidden) + (size_t)b0 * c.D * 2;
-            const bool split = z.hidden_splits > 1;
-            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, rows, z.ld, z.ld, ce::kTileM / 2));
+            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, padded, z.ld, z.ld, ce::kTileM / 2));
             CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileK));
-            if (split)
-                CE_TRY(tensor_map(&g.out, CE_F32, ws.hidden_parts,
-                                  z.hidden_slab * z.hidden_splits, c.D, c.D, 32));
-            else
-                CE_TRY(tensor_map(&g.out, c.dtype, dh, rows, c.D, c.D, 32));
-            g.tiles_m = (int)ceil_div(rows, ce::kTileM);
-            g.tiles_n = (int)ceil_div(c.D, ce::kTileN);
-            g.splits = z.hidden_splits;
-            g.k_blocks = (int)ceil_div(c.C, ce::kTileK);
-            g.group_m = std::min(g.tiles_m, 8);
-            g.split_rows = z.hidden_slab;
-            g.rows = (int)rows;
-            CE_CUDA(ce::launch_head_gemm(g, ce::kProdHidden, split ? ce::kEpiF32 : ce::kEpiOut,
-                                         bf16, sms, s));
-            if (split)
-                CE_CUDA(ce::launch_head_join(ws.hidden_parts, rows * c.D, z.hidden_slab * c.D,
-                                             z.hidden_splits, &ws.info->out, 1.f, dh, bf16, sms,
-                                             s));
+            g.group_m = 8;
+            g.may_split = 1;
+            g.row_mul = z.per_row ? &ws.row->mul : nullptr;
+            g.row_mul_stride = sizeof(ce::HeadRow) / sizeof(float);
+            g.dhidden = static_cast<unsigned char *>(c.dhidden);
+            CE_CUDA(ce::launch_head_gemm(g, ce::kProdHidden, ce::kEpiOut, bf16, pairs, s));
+            CE_CUDA(ce::launch_head_join(g, ce::kProdHidden, c.dhidden, bf16, pairs, s));
         }
         if (c.dweight) {
-            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, rows, z.ld, z.ld, ce::kTileK));
-            CE_TRY(tensor_map(&g.b, c.dtype, h, rows, c.D, c.D, ce::kTileK));
+            if (z.per_row) CE_CUDA(ce::launch_head_scale_hidden(r, s));
+            CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, padded, z.ld, z.ld, ce::kTileK));
+            if (z.per_row) {
+                CE_TRY(tensor_map(&g.b, c.dtype, ws.scaled, padded, c.D, c.D, ce::kTileK));
+                g.packed = g.b;
+            } else {
+                CE_TRY(tensor_map(&g.b, c.dtype, h, rows, c.D, c.D, ce::kTileK));
+                CE_TRY(tensor_map(&g.packed, c.dtype, hp, padded, c.D, c.D, ce::kTileK));
+            }
             if (z.weight_f32)
-                CE_TRY(tensor_map(&g.out, CE_F32, ws.weight_parts,
-                                  z.weight_slab * z.weight_splits, c.D, c.D, 32));
+                CE_TRY(tensor_map(&g.out, CE_F32, ws.weight, c.C, c.D, c.D, 32));
             else
                 CE_TRY(tensor_map(&g.out, c.dtype, c.dweight, c.C, c.D, c.D, 32));
-            g.tiles_m = (int)z.tiles;
-            g.tiles_n = (int)ceil_div(c.D, ce::kTileN);
-            g.k_blocks = (int)ceil_div(rows, ce::kTileK);
-            g.splits = z.weight_splits;
-            g.group_m = std::min(g.tiles_m, 8);
-            g.split_rows = z.weight_slab;
-            g.rows = (int)c.C;
+            g.group_m = 8;
+            g.may_split = !z.weight_f32;
             CE_CUDA(ce::launch_head_gemm(g, ce::kProdWeight,
                                          !z.weight_f32 ? ce::kEpiOut
                                          : i == 0      ? ce::kEpiF32
                                                        : ce::kEpiAdd,
-                                         bf16, sms, s));
+                                         bf16, pairs, s));
+            if (!z.weight_f32)
+                CE_CUDA(ce::launch_head_join(g, ce::kProdWeight, c.dweight, bf16, pairs, s));
         }
     }
     if (c.dweight && z.weight_f32)
-        CE_CUDA(ce::launch_head_join(ws.weight_parts, c.C * c.D, z.weight_slab * c.D,
-                                     z.weight_splits, &ws.info->out, 1.f, c.dweight, bf16, sms, s));
-    if (!none || grad)
-        CE_CUDA(ce::launch_head_loss(loss_rows, c.B, c.reduction, ws.info, c.loss, s));
+        CE_CUDA(ce::launch_head_convert(ws.weight, c.C * c.D, ws.info, 1.f, c.dweight, bf16, sms,
+                                        s));
+    if (!none || z.grad)
+        CE_CUDA(ce::launch_head_loss(loss_rows, c.B, c.reduction, teacher, ws.info, c.loss, s));
     return CE_OK;
 }
 

@@ -12,9 +12,8 @@
 // formed (two accumulators of 256 columns: all of tensor memory).
 //
 // The logits never leave the SM as logits: their epilogue turns a tile into
-// its rows' maximum and sum of exponentials (without the target's class, whose
-// logit is kept in fp32), and, when gradients follow, into 16-bit exponentials
-// relative to the tile's maximum.
+// its rows' maximum and sum of exponentials (without the target's class), and,
+// when gradients follow, into 16-bit exponentials.
 #include <math.h>
 
 #include "ce_head_gemm.h"
@@ -45,28 +44,25 @@ struct Barriers {
 constexpr int kSmemBytes =
     kStages * kStageBytes + 4 * kEpiBufs * kEpiBufBytes + 1024 /* alignment */ + sizeof(Barriers);
 
-// The tile and part of work unit u: groups of group_m tile rows, walked down
-// the columns of the group, so that neighbouring pairs share operands in L2.
+// Work unit u: a tile, and the part [k0, k1) of its contraction.
 struct Unit {
-    int mt, nt, split;
+    int mt, nt, k0, k1;
+    int part;  // -1: all of it, else the part's place among the parts
 };
-__device__ __forceinline__ Unit unit_of(const HeadGemm &p, int u) {
+__device__ __forceinline__ Unit unit_of(const HeadGemm &p, const HeadWork &w, int u) {
     Unit r;
-    const int tiles = p.tiles_m * p.tiles_n;
-    r.split = u / tiles;
-    u -= r.split * tiles;
-    const int per_group = p.group_m * p.tiles_n;
-    const int g = u / per_group;
-    u -= g * per_group;
-    const int first = g * p.group_m;
-    const int gm = min(p.group_m, p.tiles_m - first);
-    r.nt = u / gm;
-    r.mt = first + (u - r.nt * gm);
+    int tile = u, split = 0, splits = 1;
+    r.part = -1;
+    if (u >= w.full) {
+        r.part = u - w.full;
+        splits = w.splits;
+        tile = w.full + r.part / splits;
+        split = r.part % splits;
+    }
+    head_tile(p, w, tile, &r.mt, &r.nt);
+    r.k0 = (int)((long long)w.k_blocks * split / splits);
+    r.k1 = (int)((long long)w.k_blocks * (split + 1) / splits);
     return r;
-}
-__device__ __forceinline__ void k_range(const HeadGemm &p, int split, int &k0, int &k1) {
-    k0 = (int)((long long)p.k_blocks * split / p.splits);
-    k1 = (int)((long long)p.k_blocks * (split + 1) / p.splits);
 }
 
 // 16 bytes of row `row` of a 128-byte wide staging box, in TMA's 128-byte
@@ -110,92 +106,200 @@ struct Stager {
     }
 };
 
-template <typename E>
-__device__ __forceinline__ void epi_logits(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                           Stager &st) {
+// The staged box (32 rows of 128 bytes) to 32 rows of a row-major matrix, 16
+// bytes per lane: rows `at` (each lane's own row's address, nullptr: none),
+// as many of their bytes as are inside.
+__device__ __forceinline__ void unstage(const unsigned char *box, unsigned char *at, int bytes) {
     const int lane = threadIdx.x & 31;
-    const int row = m0 + lane;
-    const int n0 = u.nt * kTileN;
-    const int cols = min(kTileN, p.cols - n0);
-    int t = -1;
-    if (p.targets != nullptr && row < p.rows) t = __ldg(p.targets + row) - n0;
-    if (t >= cols) t = -1;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), piece = lane & 7;
+        unsigned char *dst = reinterpret_cast<unsigned char *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), r));
+        if (dst != nullptr && piece * 16 < bytes)
+            *reinterpret_cast<uint4 *>(dst + piece * 16) =
+                *reinterpret_cast<const uint4 *>(box + r * 128 + ((piece ^ (r & 7)) << 4));
+    }
+    __syncwarp();
+}
+
+// Row m0 + lane of this piece, and its target's column in this tile (-1:
+// elsewhere, or none).
+struct LogitRow {
+    int row, target;
+    bool counts;
+};
+__device__ __forceinline__ LogitRow logit_row(const HeadGemm &p, const HeadWork &w, int m0, int n0,
+                                              int cols) {
+    LogitRow r;
+    r.row = m0 + (threadIdx.x & 31);
+    r.counts = r.row < w.rows;
+    r.target = -1;
+    if (p.targets != nullptr && r.counts) {
+        const int at = p.first + r.row;
+        r.target = __ldg(p.targets + (p.perm ? p.perm[at] : at)) - n0;
+        if (r.target >= cols) r.target = -1;
+    }
+    return r;
+}
+
+// Columns c .. c + 31 of a tile of `cols`, the target and what lies outside
+// read as -inf.
+__device__ __forceinline__ void load_logits(float (&v)[32], uint32_t acc, int c, int cols,
+                                            const LogitRow &r) {
+    tmem_ld32(acc + c, v);
+    tmem_wait_ld(v);
+    if ((unsigned)(r.target - c) < 32u) put(v, r.target - c, -INFINITY);
+    if (c + 32 > cols) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c + i >= cols) v[i] = -INFINITY;
+    }
+}
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+    float a = v[0], b = v[1];
+#pragma unroll
+    for (int i = 2; i < 32; i += 2) {
+        a = fmaxf(a, v[i]);
+        b = fmaxf(b, v[i + 1]);
+    }
+    return fmaxf(a, b);
+}
+// 2^(v exp_scale - M) of 32 logits: added to `sum`, and (KEEP) staged as
+// pieces piece0 .. of this lane's row.
+template <typename E, bool KEEP>
+__device__ __forceinline__ void exponentials(const float (&v)[32], float exp_scale, float M,
+                                             unsigned long long &sum, unsigned char *box,
+                                             int piece0, bool zero) {
+    const unsigned long long sc2 = f2_pack(exp_scale, exp_scale), nM2 = f2_pack(-M, -M);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        unsigned long long e2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]), sc2, nM2), a, b);
+            e2[i] = f2_pack(ex2(a), ex2(b));
+            sum = f2_add(sum, e2[i]);
+        }
+        if (KEEP)
+            stage16(box, threadIdx.x & 31, piece0 + q,
+                    zero ? make_uint4(0u, 0u, 0u, 0u) : E::pack2(e2));
+    }
+}
+
+// The tile's maxima first, then its exponentials relative to them: (M, S) with
+// the tile's sum of exponentials S 2^M.
+template <typename E, bool KEEP>
+__device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &w, const Unit &u,
+                                             uint32_t acc, int m0, Stager &st) {
+    const int n0 = u.nt * p.tile_n;
+    const int cols = min(p.tile_n, p.C - n0);
+    const LogitRow r = logit_row(p, w, m0, n0, cols);
     float v[32];
-    // the tile's maximum, the target left out
     float m = -INFINITY;
     for (int c = 0; c < cols; c += 32) {
         tmem_ld32(acc + c, v);
         tmem_wait_ld(v);
-        if ((unsigned)(t - c) < 32u) {
-            p.zt[row] = pick(v, t - c);
-            put(v, t - c, -INFINITY);
+        if ((unsigned)(r.target - c) < 32u) {
+            p.zt[r.row] = pick(v, r.target - c);
+            put(v, r.target - c, -INFINITY);
         }
         if (c + 32 > cols) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (c + i >= cols) v[i] = -INFINITY;
         }
-        float a = v[0], b = v[1];
-#pragma unroll
-        for (int i = 2; i < 32; i += 2) {
-            a = fmaxf(a, v[i]);
-            b = fmaxf(b, v[i + 1]);
-        }
-        m = fmaxf(m, fmaxf(a, b));
+        m = fmaxf(m, max32(v));
     }
-    // e^(z / T) = 2^(z exp_scale - M), M the fp32 value all of the tile uses
     const float M = m == -INFINITY ? 0.f : m * p.exp_scale - p.shift;
-    const unsigned long long sc2 = f2_pack(p.exp_scale, p.exp_scale);
-    const unsigned long long nM2 = f2_pack(-M, -M);
-    unsigned long long sum2 = 0ull;
+    unsigned long long sum = 0ull;
     for (int c0 = 0; c0 < cols; c0 += 64) {
-        unsigned char *box = nullptr;
-        if (p.write_exp) box = st.open();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = c0 + 32 * h;
-            tmem_ld32(acc + c, v);
-            tmem_wait_ld(v);
-            if ((unsigned)(t - c) < 32u) put(v, t - c, -INFINITY);
-            if (c + 32 > cols) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (c + i >= cols) v[i] = -INFINITY;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                unsigned long long e2[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float a, b;
-                    f2_unpack(f2_fma(f2_pack(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]), sc2, nM2), a,
-                              b);
-                    e2[i] = f2_pack(ex2(a), ex2(b));
-                    sum2 = f2_add(sum2, e2[i]);
-                }
-                if (p.write_exp) stage16(box, lane, 4 * h + q, E::pack2(e2));
-            }
-        }
-        if (p.write_exp) {
-            st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
-        }
+        unsigned char *box = KEEP ? st.open() : nullptr;
+        load_logits(v, acc, c0, cols, r);
+        exponentials<E, KEEP>(v, p.exp_scale, M, sum, box, 0, !r.counts);
+        load_logits(v, acc, c0 + 32, cols, r);
+        exponentials<E, KEEP>(v, p.exp_scale, M, sum, box, 4, !r.counts);
+        if (KEEP) st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
     }
-    if (row < p.rows) {
+    if (r.counts) {
         float a, b;
-        f2_unpack(sum2, a, b);
-        p.stats[(size_t)u.nt * p.rows + row] =
-            make_float2(m == -INFINITY ? -INFINITY : M, a + b);
+        f2_unpack(sum, a, b);
+        p.stats[(size_t)u.nt * p.rows + r.row] = make_float2(m == -INFINITY ? -INFINITY : M, a + b);
     }
 }
 
+// Exponentials relative to the row's given exponent, in one pass: (m, S) with
+// the tile's largest exponent m and its sum of exponentials S 2^ref.
 template <typename E>
-__device__ __forceinline__ void epi_out(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                        float f, Stager &st) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void epi_ref(const HeadGemm &p, const HeadWork &w, const Unit &u,
+                                        uint32_t acc, int m0, Stager &st) {
+    const int n0 = u.nt * kTileN;
+    const int cols = min(kTileN, p.C - n0);
+    const LogitRow r = logit_row(p, w, m0, n0, cols);
+    const float M = r.counts ? p.ref[r.row] : 0.f;
     float v[32];
-#pragma unroll 1
-    for (int c0 = 0; c0 < min(kTileN, p.cols - u.nt * kTileN); c0 += 64) {
+    float m = -INFINITY;
+    unsigned long long sum = 0ull;
+    for (int c0 = 0; c0 < cols; c0 += 64) {
         unsigned char *box = st.open();
+        load_logits(v, acc, c0, cols, r);
+        m = fmaxf(m, max32(v));
+        exponentials<E, true>(v, p.exp_scale, M, sum, box, 0, !r.counts);
+        load_logits(v, acc, c0 + 32, cols, r);
+        m = fmaxf(m, max32(v));
+        exponentials<E, true>(v, p.exp_scale, M, sum, box, 4, !r.counts);
+        st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
+    }
+    if (r.counts) {
+        float a, b;
+        f2_unpack(sum, a, b);
+        p.stats[(size_t)u.nt * p.rows + r.row] = make_float2(m * p.exp_scale, a + b);
+    }
+}
+
+// A part of a tile in fp32 to its place among the parts.
+__device__ __forceinline__ void epi_part(const HeadGemm &p, const Unit &u, uint32_t acc, int row0,
+                                         Stager &st) {
+    const int lane = threadIdx.x & 31;
+    float *at = p.parts + (size_t)u.part * (kTileM * kTileN) + (size_t)(row0 + lane) * kTileN;
+    float v[32];
+    if (lane == 0) bulk_wait_read<0>();  // a store of the tile before may still read the box
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < kTileN; c += 32) {
+        unsigned char *box = st.base;
+        tmem_ld32(acc + c, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float x[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            stage16(box, lane, q, Elem<float>::pack(x));
+        }
+        unstage(box, reinterpret_cast<unsigned char *>(at + c), 128);
+    }
+}
+
+// The hidden states' gradient: row i's sum times its own factor, to its
+// place in the call's batch.
+template <typename E>
+__device__ __forceinline__ void epi_hidden(const HeadGemm &p, const HeadWork &w, const Unit &u,
+                                           uint32_t acc, int m0, float f, Stager &st) {
+    const int lane = threadIdx.x & 31;
+    const int row = m0 + lane;
+    const bool counts = row < w.rows;
+    unsigned char *at = nullptr;
+    if (counts) {
+        if (p.row_mul) f *= p.row_mul[(size_t)row * p.row_mul_stride];
+        const int b = p.perm ? p.perm[p.first + row] : p.first + row;
+        at = p.dhidden + (size_t)b * p.D * 2;
+    }
+    float v[32];
+    const int cols = min(kTileN, p.D - u.nt * kTileN);
+#pragma unroll 1
+    for (int c0 = 0; c0 < cols; c0 += 64) {
+        unsigned char *box = st.base;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             tmem_ld32(acc + c0 + 32 * h, v);
@@ -208,31 +312,58 @@ __device__ __forceinline__ void epi_out(const HeadGemm &p, const Unit &u, uint32
                 stage16(box, lane, 4 * h + q, E::pack(x));
             }
         }
+        unstage(box, at ? at + (size_t)(u.nt * kTileN + c0) * 2 : nullptr, (cols - c0) * 2);
+    }
+}
+
+// The weights' gradient in 16 bits (`zero`: no row counts).
+template <typename E>
+__device__ __forceinline__ void epi_weight(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
+                                           float f, bool zero, Stager &st) {
+    const int lane = threadIdx.x & 31;
+    float v[32];
+    const int cols = min(kTileN, p.D - u.nt * kTileN);
+#pragma unroll 1
+    for (int c0 = 0; c0 < cols; c0 += 64) {
+        unsigned char *box = st.open();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            tmem_ld32(acc + c0 + 32 * h, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : f * v[8 * q + i];
+                stage16(box, lane, 4 * h + q, E::pack(x));
+            }
+        }
         st.close([&](const void *src) { tma_store(&p.out, src, u.nt * kTileN + c0, m0); });
     }
 }
 
+// The weights' gradient in fp32, over several pieces of the rows.
 template <bool ADD>
 __device__ __forceinline__ void epi_f32(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                        Stager &st) {
+                                        bool zero, Stager &st) {
     const int lane = threadIdx.x & 31;
-    const int y = (int)(u.split * p.split_rows) + m0;
     float v[32];
+    const int cols = min(kTileN, p.D - u.nt * kTileN);
 #pragma unroll 1
-    for (int c = 0; c < min(kTileN, p.cols - u.nt * kTileN); c += 32) {
+    for (int c = 0; c < cols; c += 32) {
         unsigned char *box = st.open();
         tmem_ld32(acc + c, v);
         tmem_wait_ld(v);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float x[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-            stage16(box, lane, q, Elem<float>::pack(x));
+            stage16(box, lane, q, zero ? make_uint4(0u, 0u, 0u, 0u) : Elem<float>::pack(x));
         }
         st.close([&](const void *src) {
             if (ADD)
-                tma_add(&p.out, src, u.nt * kTileN + c, y);
+                tma_add(&p.out, src, u.nt * kTileN + c, m0);
             else
-                tma_store(&p.out, src, u.nt * kTileN + c, y);
+                tma_store(&p.out, src, u.nt * kTileN + c, m0);
         });
     }
 }
@@ -254,7 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr bool kAMn = PROD == kProdWeight;
     constexpr bool kBMn = PROD != kProdLogits;
     constexpr bool kBf16 = E::kNegInfWord == Elem<__nv_bfloat16>::kNegInfWord;
-    constexpr uint32_t kIdesc = instr_desc(kBf16, kAMn, kBMn, kTileM, kTileN);
     extern __shared__ unsigned char smem_raw[];
     // 1024-byte aligned (a swizzle atom), at the same offset in both CTAs
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -266,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
     const int pairs = gridDim.x >> 1;
-    const int units = p.tiles_m * p.tiles_n * p.splits;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -281,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         prefetch_map(&p.a);
         prefetch_map(&p.b);
         prefetch_map(&p.out);
+        prefetch_map(&p.packed);
     }
     if (warp == 2) tmem_alloc_pair(&bar.tmem, kTmemCols);
     tc_fence_before();
@@ -289,8 +419,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&bar.tmem);
     pdl_trigger();
     pdl_wait();
-    if (p.clear_failed && blockIdx.x == 0 && threadIdx.x == 0)
-        *reinterpret_cast<volatile int *>(p.failed) = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (p.clear_failed) *reinterpret_cast<volatile int *>(p.failed) = 0;
+        if (p.clear_rescue) *reinterpret_cast<volatile int *>(p.rescue) = 0;
+    }
+    const bool skip = p.only_if != nullptr && *reinterpret_cast<const volatile int *>(p.only_if) == 0;
+    const int count = p.dynamic ? p.info->count : p.B;
+    const bool packed = count < p.B;
+    const HeadWork work = head_work(p, (HeadProduct)PROD, count, pairs);
+    const int units = skip || (EPI == kEpiAdd && work.rows == 0) ? 0 : work.units;
+    // the operand that is the hidden states (logits: A; weights: B)
+    const CUtensorMap *map_a = PROD == kProdLogits && packed ? &p.packed : &p.a;
+    const CUtensorMap *map_b = PROD == kProdWeight && packed ? &p.packed : &p.b;
+    const int half_n = p.tile_n / 2;  // rows of B per CTA
 
     if (warp == 0 && lane == 0) {
         // ---- the producer: this CTA's halves of A and B
@@ -298,28 +439,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t ph = 0;
         bool ok = true;
         for (int w = pair; ok && w < units; w += pairs) {
-            const Unit u = unit_of(p, w);
+            const Unit u = unit_of(p, work, w);
             const int m0 = u.mt * kTileM + rank * kCtaRows;
-            const int n0 = u.nt * kTileN + rank * kCtaRows;
-            int k0, k1;
-            k_range(p, u.split, k0, k1);
-            for (int k = k0; k < k1; ++k) {
+            const int n0 = u.nt * p.tile_n + rank * half_n;
+            for (int k = u.k0; k < u.k1; ++k) {
                 if (!(ok = wait_or_fail(p, &bar.empty[s], ph ^ 1u))) break;
-                if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
+                if (rank == 0)
+                    mbar_arrive_expect_tx(&bar.full[s], 2 * (kOperandBytes + half_n * kTileK * 2));
                 const uint32_t fb = mapa(&bar.full[s], 0);
                 unsigned char *da = smem + s * kStageBytes;
                 unsigned char *db = da + kOperandBytes;
                 if constexpr (kAMn) {
-                    tma_load_pair(da, &p.a, m0, k * kTileK, fb);
-                    tma_load_pair(da + kOperandBytes / 2, &p.a, m0 + 64, k * kTileK, fb);
+                    tma_load_pair(da, map_a, m0, k * kTileK, fb);
+                    tma_load_pair(da + kOperandBytes / 2, map_a, m0 + 64, k * kTileK, fb);
                 } else {
-                    tma_load_pair(da, &p.a, k * kTileK, m0, fb);
+                    tma_load_pair(da, map_a, k * kTileK, m0, fb);
                 }
                 if constexpr (kBMn) {
-                    tma_load_pair(db, &p.b, n0, k * kTileK, fb);
-                    tma_load_pair(db + kOperandBytes / 2, &p.b, n0 + 64, k * kTileK, fb);
+                    tma_load_pair(db, map_b, n0, k * kTileK, fb);
+                    tma_load_pair(db + kOperandBytes / 2, map_b, n0 + 64, k * kTileK, fb);
                 } else {
-                    tma_load_pair(db, &p.b, k * kTileK, n0, fb);
+                    tma_load_pair(db, map_b, k * kTileK, n0, fb);
                 }
                 ++issued;
                 if (++s == kStages) {
@@ -340,19 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---- the matrix instructions of the pair
+        const uint32_t idesc = instr_desc(kBf16, kAMn, kBMn, kTileM, p.tile_n);
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         int it = 0;
         for (int w = pair; ok && w < units; w += pairs, ++it) {
-            const Unit u = unit_of(p, w);
-            int k0, k1;
-            k_range(p, u.split, k0, k1);
+            const Unit u = unit_of(p, work, w);
             const int ab = it & 1;
             if (!(ok = wait_or_fail(p, &bar.acc_empty[ab], ((it >> 1) & 1) ^ 1))) break;
             tc_fence_after();
             const uint32_t d = tmem + ab * kTileN;
-            for (int k = k0; k < k1; ++k) {
+            for (int k = u.k0; k < u.k1; ++k) {
                 if (!(ok = wait_or_fail(p, &bar.full[s], ph))) break;
                 tc_fence_after();
                 const uint32_t a = smem_addr(smem + s * kStageBytes);
@@ -363,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                              : smem_desc(a + kk * 32, 16, 1024);
                     const uint64_t bd = kBMn ? smem_desc(b + kk * 2048, kOperandBytes / 2, 1024)
                                              : smem_desc(b + kk * 32, 16, 1024);
-                    mma_pair(d, ad, bd, kIdesc, k > k0 || kk > 0);
+                    mma_pair(d, ad, bd, idesc, k > u.k0 || kk > 0);
                 }
                 commit_pair(&bar.empty[s]);
                 if (++s == kStages) {
@@ -380,22 +519,37 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         st.base = boxes + (warp - kEpiWarp0) * kEpiBufs * kEpiBufBytes;
         st.n = 0;
         float f = 1.f;
-        if constexpr (EPI == kEpiOut) f = p.alpha * (p.scale ? __ldg(p.scale) : 1.f);
+        if constexpr (EPI == kEpiOut) f = p.alpha * p.info->out;
         // a whole contraction may lie between two finished accumulators
-        const long long acc_limit = kWaitLimitCycles + 4096LL * p.k_blocks;
+        const long long acc_limit = kWaitLimitCycles + 4096LL * work.k_blocks;
+        // rows of the product; of the logits also those up to the next 64,
+        // whose kept exponentials are zeros (the last stage of E^T H reads them)
+        const int rows = PROD == kProdWeight ? p.C
+                         : PROD == kProdLogits ? (work.rows + 63) / 64 * 64 : work.rows;
+        const bool zero = work.k_blocks == 0;
         int it = 0;
         for (int w = pair; w < units; w += pairs, ++it) {
-            const Unit u = unit_of(p, w);
+            const Unit u = unit_of(p, work, w);
             const int ab = it & 1;
             if (!wait_or_fail(p, &bar.acc_full[ab], (it >> 1) & 1, acc_limit)) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN;
-            const int m0 = u.mt * kTileM + rank * kCtaRows + quad * 32;
-            if (m0 < p.rows) {
-                if constexpr (EPI == kEpiLogits) epi_logits<E>(p, u, acc, m0, st);
-                if constexpr (EPI == kEpiOut) epi_out<E>(p, u, acc, m0, f, st);
-                if constexpr (EPI == kEpiF32) epi_f32<false>(p, u, acc, m0, st);
-                if constexpr (EPI == kEpiAdd) epi_f32<true>(p, u, acc, m0, st);
+            const int row0 = rank * kCtaRows + quad * 32;
+            const int m0 = u.mt * kTileM + row0;
+            if (m0 < rows) {
+                if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, st);
+                if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, st);
+                if constexpr (EPI == kEpiRef) epi_ref<E>(p, work, u, acc, m0, st);
+                if constexpr (EPI == kEpiOut) {
+                    if (u.part >= 0)
+                        epi_part(p, u, acc, row0, st);
+                    else if constexpr (PROD == kProdHidden)
+                        epi_hidden<E>(p, work, u, acc, m0, f, st);
+                    else
+                        epi_weight<E>(p, u, acc, m0, f, zero, st);
+                }
+                if constexpr (EPI == kEpiF32) epi_f32<false>(p, u, acc, m0, zero, st);
+                if constexpr (EPI == kEpiAdd) epi_f32<true>(p, u, acc, m0, zero, st);
             }
             tc_fence_before();
             __syncwarp();
@@ -411,45 +565,147 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == 2) tmem_free_pair(tmem, kTmemCols);
 }
 
-template <int PROD, int EPI, typename T>
-cudaError_t launch_t(const HeadGemm &p, int sms, cudaStream_t s) {
-    const void *f = reinterpret_cast<const void *>(head_gemm_kernel<PROD, EPI, T>);
-    cudaError_t e = ensure_smem_attr(f, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    const long long units = (long long)p.tiles_m * p.tiles_n * p.splits;
-    const long long pairs = units < sms / 2 ? units : sms / 2;
+// ------------------------------------------------------------- the parts
+// A warp per row of a split tile: its parts added in order.
+template <int PROD, typename T>
+__global__ void __launch_bounds__(256)
+    head_join_kernel(const __grid_constant__ HeadGemm p, unsigned char *out, int pairs) {
+    using E = Elem<T>;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const HeadWork work =
+        head_work(p, (HeadProduct)PROD, p.dynamic ? p.info->count : p.B, pairs);
+    const int m_rows = PROD == kProdWeight ? p.C : work.rows;
+    const float f0 = p.alpha * p.info->out;
+    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < work.rest * kTileM; i += gridDim.x * 8) {
+        const int r = i / kTileM, y = i % kTileM;
+        int mt, nt;
+        head_tile(p, work, work.full + r, &mt, &nt);
+        const int row = mt * kTileM + y, col = nt * kTileN + lane * 8;
+        if (row >= m_rows || col >= p.D) continue;
+        const float *src = p.parts + (size_t)r * work.splits * (kTileM * kTileN) +
+                           (size_t)y * kTileN + lane * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int q = 0; q < work.splits; ++q) {
+            const float4 a = __ldcg(reinterpret_cast<const float4 *>(src));
+            const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + 4));
+            src += kTileM * kTileN;
+            v[0] += a.x;
+            v[1] += a.y;
+            v[2] += a.z;
+            v[3] += a.w;
+            v[4] += b.x;
+            v[5] += b.y;
+            v[6] += b.z;
+            v[7] += b.w;
+        }
+        float f = f0;
+        size_t at = row;
+        if (PROD == kProdHidden) {
+            if (p.row_mul) f *= p.row_mul[(size_t)row * p.row_mul_stride];
+            at = p.perm ? p.perm[p.first + row] : p.first + row;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= f;
+        *reinterpret_cast<uint4 *>(out + (at * p.D + col) * 2) = E::pack(v);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    head_convert_kernel(const float *parts, long long n, const HeadInfo *info, float alpha,
+                        unsigned char *out) {
+    using E = Elem<T>;
+    pdl_trigger();
+    pdl_wait();
+    const float f = alpha * info->out;
+    const long long step = (long long)gridDim.x * 256 * 8;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(parts + i));
+        const float4 b = __ldcg(reinterpret_cast<const float4 *>(parts + i + 4));
+        const float v[8] = {f * a.x, f * a.y, f * a.z, f * a.w, f * b.x, f * b.y, f * b.z, f * b.w};
+        *reinterpret_cast<uint4 *>(out + i * 2) = E::pack(v);
+    }
+}
+
+cudaLaunchConfig_t config(unsigned ctas, unsigned threads, size_t smem, cudaStream_t s,
+                          cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int PROD, int EPI, typename T>
+cudaError_t launch_t(const HeadGemm &p, int pairs, cudaStream_t s) {
+    const void *f = reinterpret_cast<const void *>(head_gemm_kernel<PROD, EPI, T>);
+    cudaError_t e = ensure_smem_attr(f, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config((unsigned)(2 * pairs), kThreads, kSmemBytes, s, attr);
     return cudaLaunchKernelEx(&cfg, head_gemm_kernel<PROD, EPI, T>, p);
 }
 
 template <typename T>
-cudaError_t launch_of(const HeadGemm &p, HeadProduct prod, HeadEpilogue epi, int sms,
+cudaError_t launch_of(const HeadGemm &p, HeadProduct prod, HeadEpilogue epi, int pairs,
                       cudaStream_t s) {
-    if (prod == kProdLogits && epi == kEpiLogits)
-        return launch_t<kProdLogits, kEpiLogits, T>(p, sms, s);
-    if (prod == kProdHidden && epi == kEpiOut) return launch_t<kProdHidden, kEpiOut, T>(p, sms, s);
-    if (prod == kProdHidden && epi == kEpiF32) return launch_t<kProdHidden, kEpiF32, T>(p, sms, s);
-    if (prod == kProdWeight && epi == kEpiOut) return launch_t<kProdWeight, kEpiOut, T>(p, sms, s);
-    if (prod == kProdWeight && epi == kEpiF32) return launch_t<kProdWeight, kEpiF32, T>(p, sms, s);
-    if (prod == kProdWeight && epi == kEpiAdd) return launch_t<kProdWeight, kEpiAdd, T>(p, sms, s);
+    if (prod == kProdLogits && epi == kEpiStats)
+        return launch_t<kProdLogits, kEpiStats, T>(p, pairs, s);
+    if (prod == kProdLogits && epi == kEpiKeep)
+        return launch_t<kProdLogits, kEpiKeep, T>(p, pairs, s);
+    if (prod == kProdLogits && epi == kEpiRef)
+        return launch_t<kProdLogits, kEpiRef, T>(p, pairs, s);
+    if (prod == kProdHidden && epi == kEpiOut)
+        return launch_t<kProdHidden, kEpiOut, T>(p, pairs, s);
+    if (prod == kProdWeight && epi == kEpiOut)
+        return launch_t<kProdWeight, kEpiOut, T>(p, pairs, s);
+    if (prod == kProdWeight && epi == kEpiF32)
+        return launch_t<kProdWeight, kEpiF32, T>(p, pairs, s);
+    if (prod == kProdWeight && epi == kEpiAdd)
+        return launch_t<kProdWeight, kEpiAdd, T>(p, pairs, s);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_head_gemm(const HeadGemm &p, HeadProduct prod, HeadEpilogue epi, bool bf16,
-                             int sms, cudaStream_t s) {
-    return bf16 ? launch_of<__nv_bfloat16>(p, prod, epi, sms, s)
-                : launch_of<__half>(p, prod, epi, sms, s);
+                             int pairs, cudaStream_t s) {
+    return bf16 ? launch_of<__nv_bfloat16>(p, prod, epi, pairs, s)
+                : launch_of<__half>(p, prod, epi, pairs, s);
+}
+
+cudaError_t launch_head_join(const HeadGemm &p, HeadProduct prod, void *out, bool bf16, int pairs,
+                             cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config((unsigned)(8 * pairs), 256, 0, s, attr);
+    unsigned char *o = static_cast<unsigned char *>(out);
+    if (prod == kProdHidden)
+        return bf16 ? cudaLaunchKernelEx(&cfg, head_join_kernel<kProdHidden, __nv_bfloat16>, p, o,
+                                         pairs)
+                    : cudaLaunchKernelEx(&cfg, head_join_kernel<kProdHidden, __half>, p, o, pairs);
+    return bf16 ? cudaLaunchKernelEx(&cfg, head_join_kernel<kProdWeight, __nv_bfloat16>, p, o,
+                                     pairs)
+                : cudaLaunchKernelEx(&cfg, head_join_kernel<kProdWeight, __half>, p, o, pairs);
+}
+
+cudaError_t launch_head_convert(const float *parts, long long n, const HeadInfo *info, float alpha,
+                                void *out, bool bf16, int sms, cudaStream_t s) {
+    long long ctas = (n / 8 + 255) / 256;
+    if (ctas > 16LL * sms) ctas = 16LL * sms;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config((unsigned)ctas, 256, 0, s, attr);
+    unsigned char *o = static_cast<unsigned char *>(out);
+    return bf16 ? cudaLaunchKernelEx(&cfg, head_convert_kernel<__nv_bfloat16>, parts, n, info,
+                                     alpha, o)
+                : cudaLaunchKernelEx(&cfg, head_convert_kernel<__half>, parts, n, info, alpha, o);
 }
 
 }  // namespace ce

@@ -1,4 +1,5 @@
-// Host-side interface of the projection's matrix products (ce_head_gemm.cu).
+// Host-side interface of the projection's matrix products (ce_head_gemm.cu),
+// and what their kernels and the row kernels (ce_head_rows.cu) agree on.
 // Internal to the library.
 #pragma once
 
@@ -16,12 +17,23 @@ constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kTileK = 64;
 
+// What the launches of one call share on the device.
+struct HeadInfo {
+    int count;    // rows that count (not ignored, not without a list)
+    float out;    // factor of the gradients (what is not in the rows' own)
+    float norm;   // what the rows' own factors are divided by
+    int failed;   // a bounded wait gave up
+    int rescue;   // a row's reference exponent was too low
+};
+
 // What becomes of a tile.
 enum HeadEpilogue {
-    kEpiLogits = 0,  // row maxima and sums of exponentials, the exponentials in 16 bits
-    kEpiOut = 1,     // scaled, rounded to 16 bits
-    kEpiF32 = 2,     // fp32, stored (partial sums)
-    kEpiAdd = 3,     // fp32, added to what is there
+    kEpiStats = 0,  // row maxima and sums of exponentials alone
+    kEpiKeep = 1,   // these, and the exponentials relative to the tile's maxima
+    kEpiRef = 2,    // these, and the exponentials relative to a given exponent per row
+    kEpiOut = 3,    // scaled, rounded to 16 bits
+    kEpiF32 = 4,    // fp32, stored
+    kEpiAdd = 5,    // fp32, added to what is there
 };
 
 // Which way the operands lie: the logits (both rows along K), the gradient of
@@ -30,26 +42,110 @@ enum HeadProduct { kProdLogits = 0, kProdHidden = 1, kProdWeight = 2 };
 
 struct HeadGemm {
     CUtensorMap a, b, out;
-    int tiles_m, tiles_n, splits;  // output tiles, parts of the contraction
-    int k_blocks;                  // stages of the whole contraction
+    CUtensorMap packed;            // the hidden states without the rows that do not count
+    const HeadInfo *info;
+    int B;                         // rows of the call
+    int dynamic;                   // only the rows that count: [first, first + rows) of them
+    int first, rows;               // rows of this piece, at most
+    int C, D;
+    int tile_n;                    // kEpiStats: width of a tile (else kTileN)
     int group_m;                   // tile rows that are walked together
-    long long split_rows;          // output rows from one part to the next
-    const float *scale;            // kEpiOut: device factor
-    float alpha;                   //          times this
-    int rows, cols;                // of the product
-    // kEpiLogits
+    int may_split;                 // the last tiles' contraction may be split
+    float *parts;                  // fp32 tiles of the split parts (kMaxParts a pair)
+    float alpha;                   // kEpiOut: times info->out
+    // logits
     float exp_scale;               // log2(e) / temperature
-    float shift;                   // the exponentials are kept times 2^shift
-    const int32_t *targets;        // nullptr: none
-    float2 *stats;                 // [tiles_n][rows]: (M, S), sum of e^z = S 2^M over the tile
-    float *zt;                     // [rows] target logits
-    int write_exp;                 // 0: the statistics alone
-    int *failed;                   // set when a wait gave up
-    int clear_failed;              // the call's first launch clears it
+    float shift;                   // kEpiKeep: the exponentials are kept times 2^shift
+    const int32_t *targets;        // [B], nullptr: none
+    const int *perm;               // the counting rows' places, nullptr: all in order
+    float2 *stats;                 // [column tiles][rows]
+    float *zt;                     // [rows] target logits (kEpiStats, kEpiKeep)
+    const float *ref;              // [rows] reference exponents
+    const int *only_if;            // nullptr, or: nothing to do unless set
+    int clear_failed, clear_rescue;
+    // dhidden
+    const float *row_mul;          // row i's factor row_mul[i * row_mul_stride], or nullptr
+    int row_mul_stride;
+    unsigned char *dhidden;        // [B][D]
+    int *failed, *rescue;
     int *err;                      // error counters
 };
 
+// Parts of tiles whose contraction is split, at most, per pair of CTAs.
+constexpr int kMaxParts = 4;
+
+// The tiles of a product over `pairs` pairs of CTAs: whole rounds of tiles are
+// computed whole; the contraction of the `rest` tiles of the last round is
+// split into `splits` parts each, so that all pairs share them.
+struct HeadWork {
+    int rows;       // rows of this piece
+    int tiles_m, tiles_n, k_blocks;
+    int full, rest, splits, units;
+};
+__host__ __device__ inline HeadWork head_work(const HeadGemm &p, HeadProduct prod, int count,
+                                              int pairs) {
+    HeadWork w;
+    w.rows = p.rows;
+    if (p.dynamic) {
+        const int left = count - p.first;
+        w.rows = left < 0 ? 0 : left < p.rows ? left : p.rows;
+    }
+    const int m = prod == kProdWeight ? p.C : w.rows;
+    const int n = prod == kProdLogits ? p.C : p.D;
+    const int k = prod == kProdLogits ? p.D : prod == kProdHidden ? p.C : w.rows;
+    w.tiles_m = (m + kTileM - 1) / kTileM;
+    w.tiles_n = (n + p.tile_n - 1) / p.tile_n;
+    w.k_blocks = (k + kTileK - 1) / kTileK;
+    const int tiles = w.tiles_m * w.tiles_n;
+    w.full = tiles;
+    w.rest = 0;
+    w.splits = 1;
+    if (p.may_split) {
+        w.full = tiles / pairs * pairs;
+        w.rest = tiles - w.full;
+        // a stage takes about 0.35 us; a part more: its 256 KB written and read
+        // and, if there is any, a launch to add them up
+        long long best = 1LL << 60;
+        for (int s = 1; s <= 64 && w.rest > 0; ++s) {
+            if (s > 1 && (w.rest * s > kMaxParts * pairs || w.k_blocks / s < 8)) break;
+            const long long rounds = (w.rest * s + pairs - 1) / pairs;
+            const long long ns = rounds * ((w.k_blocks + s - 1) / s) * 350 +
+                                 (s > 1 ? 4000 + 80LL * w.rest * s : 0);
+            if (ns < best) {
+                best = ns;
+                w.splits = s;
+            }
+        }
+        if (w.splits == 1) {
+            w.full = tiles;
+            w.rest = 0;
+        }
+    }
+    w.units = w.full + w.rest * w.splits;
+    return w;
+}
+
+// Tile t of the walk: groups of group_m tile rows, down the columns of each,
+// so that pairs working at the same time share operands in L2.
+__host__ __device__ inline void head_tile(const HeadGemm &p, const HeadWork &w, int t, int *mt,
+                                          int *nt) {
+    const int per_group = p.group_m * w.tiles_n;
+    const int g = t / per_group;
+    t -= g * per_group;
+    const int first = g * p.group_m;
+    const int gm = p.group_m < w.tiles_m - first ? p.group_m : w.tiles_m - first;
+    *nt = t / gm;
+    *mt = first + (t - *nt * gm);
+}
+
 cudaError_t launch_head_gemm(const HeadGemm &p, HeadProduct prod, HeadEpilogue epi, bool bf16,
-                             int sms, cudaStream_t s);
+                             int pairs, cudaStream_t s);
+// The split parts of a product added up, in their order (nothing to do where
+// nothing was split).  out: dhidden's rows or the weights' gradient.
+cudaError_t launch_head_join(const HeadGemm &p, HeadProduct prod, void *out, bool bf16, int pairs,
+                             cudaStream_t s);
+// out[i] = alpha info->out parts[i], n elements (a multiple of 8), to 16 bits.
+cudaError_t launch_head_convert(const float *parts, long long n, const HeadInfo *info, float alpha,
+                                void *out, bool bf16, int sms, cudaStream_t s);
 
 }  // namespace ce

@@ -1,9 +1,15 @@
 // Row kernels around the matrix products of a vocabulary projection's loss:
-// everything that is not a matrix product.  With (M_j, S_j) the reference
-// exponent and the sum of exponentials of row b over column tile j,
-//   M = max_j M_j,  S = sum_j S_j 2^(M_j - M),
-//   p_c = E_c 2^(M_j - M) / S            (E_c the kept 16-bit exponential),
-// and the row's gradient with respect to its logits is written over E.
+// everything that is not a matrix product.  A row's statistics come per column
+// tile j, as a reference exponent M_j (log2) and the sum of exponentials S_j
+// 2^M_j.  Its exponentials E_c are kept in 16 bits relative to
+//   one exponent M per row (bf16, whose range is fp32's): a class known to be
+//     likely, the target or the teacher's best, gives it before the product;
+//     then G_c = mul E_c with one factor per row, which goes into the rows of
+//     the products' other side, and E is written and read once; or to
+//   one exponent per tile (f16): G_c = mul 2^(M_j - M) E_c, a pass over E.
+// What is kept for the target, or the listed classes, is replaced by what makes
+// their gradient exact: with S_rest the sum without the target, G_t = -mul
+// S_rest (no difference of near values is formed).
 #include <math.h>
 
 #include "ce_head_rows.h"
@@ -25,47 +31,155 @@ cudaLaunchConfig_t config(unsigned gx, unsigned gy, unsigned threads, cudaStream
     return cfg;
 }
 
-__device__ __forceinline__ float block_max_256(float v, float *scratch) {
-    v = warp_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = scratch[0];
-    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = fmaxf(v, scratch[i]);
-    return v;
+// The piece's rows that count.
+__device__ __forceinline__ int piece_rows(const HeadRows &p) {
+    if (!p.dynamic) return p.rows;
+    return min(max(p.info->count - p.first, 0), p.rows);
+}
+// The batch's row of the piece's row i.
+__device__ __forceinline__ int batch_row(const HeadRows &p, int i) {
+    return p.perm ? p.perm[p.first + i] : p.first + i;
 }
 
 // ------------------------------------------------------------------- prep
-// One CTA: the rows that count (mean), and the factors that keep the rows'
-// own gradients within [-1, 1] times the teacher's mass, so that they fit 16
-// bits whatever the upstream gradient is.
+// One CTA: the rows that count, in order, and the factors that keep the rows'
+// own gradients within [-1, 1], so that they fit 16 bits whatever the upstream
+// gradient is.
 constexpr int kPrepThreads = 1024;
 __global__ void __launch_bounds__(kPrepThreads) head_prep_kernel(HeadPrep p) {
-    __shared__ float scratch[kPrepThreads / 32];
-    __shared__ int total;
+    __shared__ float norms[32];
+    __shared__ int counts[32];
     pdl_trigger();
     pdl_wait();
-    if (threadIdx.x == 0) total = 0;
-    __syncthreads();
-    int n = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // each thread has a run of rows: their places follow from one scan
+    const long long run = (p.B + kPrepThreads - 1) / kPrepThreads;
+    const long long b0 = min(p.B, run * threadIdx.x), b1 = min(p.B, b0 + run);
+    auto counts_at = [&](long long b) {
+        return p.targets ? __ldg(p.targets + b) != p.ignore_index : p.mass[b] != 0.f;
+    };
+    int n = 0, bad = 0;
     float norm = 0.f;
-    for (long long b = threadIdx.x; b < p.B; b += kPrepThreads) {
-        const bool counts = p.targets == nullptr || __ldg(p.targets + b) != p.ignore_index;
-        n += counts;
-        float w = p.scale_per_row ? fabsf(__ldg(p.scale + b)) : 1.f;
-        if (p.mass != nullptr) w *= fmaxf(p.mass[b], 1.f);
-        norm = fmaxf(norm, w);
+    for (long long b = b0; b < b1; ++b) {
+        const bool c = counts_at(b);
+        n += c;
+        if (p.targets && c) {
+            const int t = __ldg(p.targets + b);
+            bad += t < 0 || t >= p.C;
+        }
+        if (c) {
+            float w = p.scale_per_row ? fabsf(__ldg(p.scale + b)) : 1.f;
+            if (!p.targets) w *= fmaxf(fabsf(p.mass[b]), 1.f);
+            norm = fmaxf(norm, w);
+        }
     }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&total, n);
-    norm = block_max_256(norm, scratch);
+    int before = n;  // rows of this warp's threads up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    norm = warp_max(norm);
+    if (lane == 31) {
+        counts[warp] = before;
+        norms[warp] = norm;
+    }
+    if (p.perm && bad) atomicAdd(&p.err[kErrBadTarget], bad);
     __syncthreads();
+    int base = 0, total = 0;
+    norm = 0.f;
+    for (int i = 0; i < 32; ++i) {
+        if (i < warp) base += counts[i];
+        total += counts[i];
+        norm = fmaxf(norm, norms[i]);
+    }
+    if (p.perm) {
+        int at = base + before - n;
+        for (long long b = b0; b < b1; ++b) {
+            if (counts_at(b)) {
+                p.pos[b] = at;
+                p.perm[at++] = (int)b;
+            } else {
+                p.pos[b] = -1;
+                p.loss[b] = !p.targets && signbit(p.mass[b]) ? NAN : 0.f;
+            }
+        }
+    }
     if (threadIdx.x == 0) {
         if (!(norm > 0.f) || isinf(norm)) norm = 1.f;
         const float up = p.scale != nullptr && !p.scale_per_row ? __ldg(p.scale) : 1.f;
+        const float by = p.mean_of_all ? (float)p.B : (float)max(total, 1);
         p.info->count = total;
         p.info->norm = norm;
-        p.info->out = p.alpha * norm * up * (p.mean ? 1.f / (float)max(total, 1) : 1.f);
+        p.info->out = p.alpha * norm * up * (p.mean ? 1.f / by : 1.f);
+    }
+}
+
+// ------------------------------------------------------------------- pack
+// A warp per row of the batch (and per row of padding): the hidden states of
+// the rows that count together, if not all do; zeros as the gradient of the
+// others; the logit of one likely class, whose exponent is the row's reference
+// (rounded to an integer: powers of two scale the exponentials exactly).
+template <typename T>
+__global__ void __launch_bounds__(256) head_pack_kernel(HeadPack p) {
+    using E = Elem<T>;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long b = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int count = p.info->count, nv = p.D / 8;
+    if (b >= p.B) {  // rows count .. of the last 64 are zeros
+        const long long at = count + (b - p.B);
+        if (count < p.B && at < ((long long)count + 63) / 64 * 64)
+            for (int v = lane; v < nv; v += 32)
+                reinterpret_cast<uint4 *>(p.packed + (size_t)at * p.D * 2)[v] =
+                    make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const int pos = p.pos[b];
+    if (pos < 0) {
+        if (p.dhidden)
+            for (int v = lane; v < nv; v += 32)
+                reinterpret_cast<uint4 *>(p.dhidden + (size_t)b * p.D * 2)[v] =
+                    make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const uint4 *h = reinterpret_cast<const uint4 *>(p.hidden + (size_t)b * p.D * 2);
+    uint4 *to = reinterpret_cast<uint4 *>(p.packed + (size_t)pos * p.D * 2);
+    const bool dot = p.targets != nullptr && p.ref != nullptr;
+    int c = dot ? __ldg(p.targets + b) : 0;
+    const bool has = c >= 0 && c < p.C;
+    if (!has) c = 0;  // any class: its logit is not above the largest
+    const uint4 *w = reinterpret_cast<const uint4 *>(p.weight + (size_t)c * p.D * 2);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (dot || count < p.B) {
+#pragma unroll 4
+        for (int v = lane; v < nv; v += 32) {
+            const uint4 x = __ldg(h + v);
+            if (count < p.B) to[v] = x;
+            if (dot) {
+                float a[8], y[8];
+                E::unpack(x, a);
+                E::unpack(__ldg(w + v), y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j & 3] = fmaf(a[j], y[j], acc[j & 3]);
+            }
+        }
+    }
+    if (p.ref == nullptr) return;
+    float z = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (!dot) {
+        z = -INFINITY;
+        for (int k = lane; k < p.K; k += 32) {
+            const int i = __ldg(p.idx + b * p.K + k);
+            if (i >= 0 && i < p.C) z = fmaxf(z, p.zk[b * p.K + k]);
+        }
+        z = warp_max(z);
+    }
+    if (lane == 0) {
+        const float r = rintf(z * p.exp_scale);
+        p.ref[pos] = fabsf(r) <= 1e30f ? r : 0.f;
+        if (dot) p.zt[pos] = z;
     }
 }
 
@@ -111,7 +225,7 @@ __global__ void __launch_bounds__(256) head_teacher_kernel(HeadTeacher p) {
     for (int k = lane; k < p.K; k += 32) {
         const int c = __ldg(p.idx + i0 + k);
         float lq = -INFINITY;
-        if (c >= 0 && c < p.C) {
+        if (c >= 0 && c < p.C && m != -INFINITY) {  // m = -inf: no place has a probability
             lq = (teacher_at(p, i0 + k) - m) * p.inv_t - ref;
             mass += expf(lq);
         }
@@ -120,7 +234,7 @@ __global__ void __launch_bounds__(256) head_teacher_kernel(HeadTeacher p) {
     mass = warp_sum(mass);
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-        p.mass[b] = mass;
+        p.mass[b] = bad ? -mass : mass;
         if (bad) atomicAdd(&p.err[kErrBadTarget], 1);
     }
 }
@@ -163,65 +277,100 @@ __device__ __forceinline__ MS join(MS a, MS b) {
     return {M, a.S * ex2(a.M - M) + b.S * ex2(b.M - M)};
 }
 
-template <int R>
+// Above this sum (relative to the reference exponent) the exponentials come
+// near the top of bf16's range, and their factors near its bottom.
+constexpr float kRescueSum = 1.152921504606847e18f;  // 2^60
+
+template <int R, typename T>
 __global__ void __launch_bounds__(256) head_rows_kernel(HeadRows p) {
+    using E = Elem<T>;
     constexpr int P = 256 / R;
     __shared__ MS sh[256];
     pdl_trigger();
     pdl_wait();
+    if (p.only_if != nullptr && *reinterpret_cast<const volatile int *>(p.only_if) == 0) return;
+    const int rows = piece_rows(p);
     const int r = threadIdx.x % R;
     const int part = threadIdx.x / R;
     const int row = blockIdx.x * R + r;
+    if (blockIdx.x * R >= rows) return;
+    const bool per_row = p.ref != nullptr;
     MS acc = {-INFINITY, 0.f};
-    if (row < p.rows) {
+    if (row < rows) {
         const float2 *st = p.stats + row;
+        if (per_row) {
 #pragma unroll 8
-        for (int j = part; j < p.tiles; j += P) {
-            const float2 v = __ldcg(st + (size_t)j * p.rows);
-            acc = join(acc, {v.x, v.y});
+            for (int j = part; j < p.tiles; j += P) {
+                const float2 v = __ldcg(st + (size_t)j * p.rows);
+                acc.M = fmaxf(acc.M, v.x);
+                acc.S += v.y;
+            }
+        } else {
+#pragma unroll 8
+            for (int j = part; j < p.tiles; j += P) {
+                const float2 v = __ldcg(st + (size_t)j * p.rows);
+                acc = join(acc, {v.x, v.y});
+            }
         }
     }
     sh[threadIdx.x] = acc;
 #pragma unroll
     for (int o = P / 2; o > 0; o >>= 1) {
         __syncthreads();
-        if (part < o) sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + o * R]);
+        if (part < o) {
+            const MS x = sh[threadIdx.x], y = sh[threadIdx.x + o * R];
+            sh[threadIdx.x] = per_row ? MS{fmaxf(x.M, y.M), x.S + y.S} : join(x, y);
+        }
     }
-    if (part != 0 || row >= p.rows) return;
-    const MS a = sh[threadIdx.x];
+    if (part != 0 || row >= rows) return;
+    MS a = sh[threadIdx.x];
+    const int b = batch_row(p, row);
     // the row's own factor, relative to the largest
     float w = 1.f;
-    if (p.want_grad) w = (p.row_scale ? __ldg(p.row_scale + row) : 1.f) / p.info->norm;
+    if (p.want_grad) w = (p.row_scale ? __ldg(p.row_scale + b) : 1.f) / p.info->norm;
     HeadRow out;
+    const int t = p.targets ? __ldg(p.targets + b) : -1;
+    const bool has = t >= 0 && t < p.C;
+    const float zt = has ? p.zt[row] * p.exp_scale : -INFINITY;
+    if (per_row) {
+        if (p.flag_rescue && !(a.S <= kRescueSum)) {
+            // the products are formed again with the row's largest exponent
+            const float top = ceilf(fmaxf(a.M, zt));
+            p.ref[row] = fabsf(top) <= 1e30f ? top : 0.f;
+            *reinterpret_cast<volatile int *>(&p.info->rescue) = 1;
+            return;
+        }
+        a.M = p.ref[row];
+    }
     if (p.targets != nullptr) {
-        const int t = __ldg(p.targets + row);
-        const bool has = t >= 0 && t < p.cols;
         float l;
-        if (t == p.ignore_index) {
+        if (!p.want_grad && t == p.ignore_index) {
             l = 0.f;
             out = {0.f, 0.f, 0.f, 0.f};
         } else {
-            const float zt = has ? p.zt[row] * p.exp_scale : -INFINITY;
-            out.M = fmaxf(a.M, zt);
+            out.M = per_row ? a.M : fmaxf(a.M, zt);
             const float rest = a.M == -INFINITY ? a.S : a.S * ex2(a.M - out.M);
             const float e = has ? ex2(zt - out.M) : 0.f;
             const float S = rest + e;
             l = rest < e ? log1pf(rest / e) : kLn2 * (log2f(S) - (zt - out.M));
             if (!has) {
                 l = NAN;
-                atomicAdd(&p.err[kErrBadTarget], 1);
+                if (!p.want_grad) atomicAdd(&p.err[kErrBadTarget], 1);
             }
-            out.mul = w / S * p.shift_mul;
+            out.mul = w / S * (per_row ? 1.f : p.shift_mul);
             out.target = has ? -(rest / S) * w * p.shift_mul : 0.f;
             out.log2S = log2f(S);
+            if (per_row && has)
+                E::store(p.exps + ((size_t)row * p.ld + t) * 2, -rest);
         }
         if (p.nan_on_failure && p.info->failed) l = NAN;
-        p.loss[row] = l;
+        p.loss[b] = l;
     } else {
-        const float mass = p.mass[row];
+        const float mass = fabsf(p.mass[b]);
         out.M = a.M;
-        out.mul = mass == 0.f ? 0.f : mass * w / a.S * p.shift_mul;
-        out.target = w * p.shift_mul;
+        out.mul = mass * w / a.S * (per_row ? 1.f : p.shift_mul);
+        // what a listed class's (mass p - q) is multiplied by to be kept
+        out.target = per_row ? a.S / mass : w * p.shift_mul;
         out.log2S = log2f(a.S);
     }
     p.row[row] = out;
@@ -229,8 +378,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadRows p) {
 
 // ------------------------------------------------------ kept exponentials
 // A warp per 256 columns of a row (one tile, one factor), eight of them in
-// flight; rows without a factor (ignored tokens) become zeros whatever they
-// held.
+// flight.
 constexpr int kScaleTiles = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
@@ -240,11 +388,11 @@ __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
     const int lane = threadIdx.x & 31;
     const long long groups = (p.tiles + kScaleTiles - 1) / kScaleTiles;
     const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= groups * p.rows) return;
+    if (i >= groups * piece_rows(p)) return;
     const int row = (int)(i / groups);
     const int j0 = (int)(i - row * groups) * kScaleTiles;
     const HeadRow h = p.row[row];
-    const int t = p.targets ? __ldg(p.targets + row) : -1;
+    const int t = p.targets ? __ldg(p.targets + batch_row(p, row)) : -1;
     unsigned char *base = p.exps + ((size_t)row * p.ld) * 2;
     uint4 x[kScaleTiles];
     float f[kScaleTiles];
@@ -262,15 +410,41 @@ __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
         if (c >= p.ld) continue;
         float v[8];
         E::unpack(x[k], v);
-        const bool zero = h.mul == 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = zero ? 0.f : v[e] * f[k];
-        if (t >= c && t < c + 8 && !zero) {
+        for (int e = 0; e < 8; ++e) v[e] *= f[k];
+        if (t >= c && t < c + 8) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (t - c == e) v[e] = h.target;
         }
         *reinterpret_cast<uint4 *>(base + c * 2) = E::pack(v);
+    }
+}
+
+// A warp per row (and per row of padding up to 64): h mul in bf16, for E^T h.
+__global__ void __launch_bounds__(256) head_scale_hidden_kernel(HeadRows p) {
+    using E = Elem<__nv_bfloat16>;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int rows = piece_rows(p);
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (rows + 63) / 64 * 64) return;
+    uint4 *to = reinterpret_cast<uint4 *>(p.scaled + (size_t)row * p.D * 2);
+    const unsigned char *src = p.info->count < p.B ? p.packed : p.hidden;
+    const uint4 *h = reinterpret_cast<const uint4 *>(src + (size_t)row * p.D * 2);
+    const float mul = row < rows ? p.row[row].mul : 0.f;
+#pragma unroll 4
+    for (int v = lane; v < p.D / 8; v += 32) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows) {
+            float a[8];
+            E::unpack(__ldcg(h + v), a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] *= mul;
+            x = E::pack(a);
+        }
+        to[v] = x;
     }
 }
 
@@ -285,17 +459,17 @@ __global__ void __launch_bounds__(256) head_listed_kernel(HeadRows p) {
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= p.rows) return;
+    if (row >= piece_rows(p)) return;
     const HeadRow h = p.row[row];
-    const float mass = p.mass[row];
-    const long long i0 = (long long)row * p.K;
+    const int b = batch_row(p, row);
+    const float signed_mass = p.mass[b];
+    const float mass = fabsf(signed_mass);
+    const long long i0 = (long long)b * p.K;
     float l = 0.f;
-    bool bad = false;
     for (int k = lane; k < p.K; k += 32) {
         const int c = __ldg(p.idx + i0 + k);
-        if (c < -1 || c >= p.cols) bad = true;
+        if (c < 0 || c >= p.C) continue;
         const float lq = p.logq[i0 + k];
-        if (c < 0 || c >= p.cols) continue;
         const float lp2 = p.zk[i0 + k] * p.exp_scale - h.M - h.log2S;
         const float q = expf(lq);
         if (q != 0.f) l += q * (lq - kLn2 * lp2);
@@ -313,47 +487,17 @@ __global__ void __launch_bounds__(256) head_listed_kernel(HeadRows p) {
                      (mass * ex2(lp2) - all) * h.target);
     }
     l = warp_sum(l);
-    bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-        l = bad ? NAN : l * p.temperature * p.temperature;
+        l = signbit(signed_mass) ? NAN : mass == 0.f ? 0.f : l * p.temperature * p.temperature;
         if (p.nan_on_failure && p.info->failed) l = NAN;
-        p.loss[row] = l;
-    }
-}
-
-// ------------------------------------------------------------------- join
-template <typename T>
-__global__ void __launch_bounds__(256)
-    head_join_kernel(const float *parts, long long n, long long stride, int nparts,
-                     const float *scale, float alpha, unsigned char *out) {
-    using E = Elem<T>;
-    pdl_trigger();
-    pdl_wait();
-    const float f = alpha * (scale ? *scale : 1.f);
-    const long long step = (long long)gridDim.x * 256 * 8;
-    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int q = 0; q < nparts; ++q) {
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(parts + q * stride + i));
-            const float4 b = __ldcg(reinterpret_cast<const float4 *>(parts + q * stride + i + 4));
-            v[0] += a.x;
-            v[1] += a.y;
-            v[2] += a.z;
-            v[3] += a.w;
-            v[4] += b.x;
-            v[5] += b.y;
-            v[6] += b.z;
-            v[7] += b.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        *reinterpret_cast<uint4 *>(out + i * 2) = E::pack(v);
+        p.loss[b] = l;
     }
 }
 
 // ------------------------------------------------------------------- loss
 __global__ void __launch_bounds__(kTailThreads)
-    head_loss_kernel(float *rows, long long B, int reduction, const HeadInfo *info, float *out) {
+    head_loss_kernel(float *rows, long long B, int reduction, int mean_of_all, const HeadInfo *info,
+                     float *out) {
     __shared__ float2 scratch[kTailWarps];
     pdl_trigger();
     pdl_wait();
@@ -378,7 +522,7 @@ __global__ void __launch_bounds__(kTailThreads)
             l += scratch[w].y + e;
         }
         double r = (double)h + (double)l;
-        if (reduction == kReduceMean) r /= (double)max(info->count, 1);
+        if (reduction == kReduceMean) r /= mean_of_all ? (double)B : (double)max(info->count, 1);
         *out = failed ? NAN : (float)r;
     }
 }
@@ -402,20 +546,34 @@ cudaError_t launch_head_teacher(const HeadTeacher &p, bool bf16, int sms, cudaSt
                 : cudaLaunchKernelEx(&cfg, head_dots_kernel<__half>, p);
 }
 
-cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t s) {
+cudaError_t launch_head_pack(const HeadPack &p, bool bf16, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config((unsigned)((p.B + 64 + 7) / 8), 1, 256, s, attr);
+    return bf16 ? cudaLaunchKernelEx(&cfg, head_pack_kernel<__nv_bfloat16>, p)
+                : cudaLaunchKernelEx(&cfg, head_pack_kernel<__half>, p);
+}
+
+namespace {
+template <typename T>
+cudaError_t rows_of(const HeadRows &p, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     // enough CTAs for the rows there are: 32 rows each in a large batch, one
     // each where there are few
     if (p.rows <= 256) {
         cudaLaunchConfig_t cfg = config((unsigned)p.rows, 1, 256, s, attr);
-        return cudaLaunchKernelEx(&cfg, head_rows_kernel<1>, p);
+        return cudaLaunchKernelEx(&cfg, head_rows_kernel<1, T>, p);
     }
     if (p.rows <= 2048) {
         cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 7) / 8), 1, 256, s, attr);
-        return cudaLaunchKernelEx(&cfg, head_rows_kernel<8>, p);
+        return cudaLaunchKernelEx(&cfg, head_rows_kernel<8, T>, p);
     }
     cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 31) / 32), 1, 256, s, attr);
-    return cudaLaunchKernelEx(&cfg, head_rows_kernel<32>, p);
+    return cudaLaunchKernelEx(&cfg, head_rows_kernel<32, T>, p);
+}
+}  // namespace
+
+cudaError_t launch_head_rows(const HeadRows &p, bool bf16, cudaStream_t s) {
+    return bf16 ? rows_of<__nv_bfloat16>(p, s) : rows_of<__half>(p, s);
 }
 
 cudaError_t launch_head_scale(const HeadRows &p, bool bf16, cudaStream_t s) {
@@ -426,6 +584,12 @@ cudaError_t launch_head_scale(const HeadRows &p, bool bf16, cudaStream_t s) {
                 : cudaLaunchKernelEx(&cfg, head_scale_kernel<__half>, p);
 }
 
+cudaError_t launch_head_scale_hidden(const HeadRows &p, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 63) / 64 * 8), 1, 256, s, attr);
+    return cudaLaunchKernelEx(&cfg, head_scale_hidden_kernel, p);
+}
+
 cudaError_t launch_head_listed(const HeadRows &p, bool bf16, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 7) / 8), 1, 256, s, attr);
@@ -433,25 +597,12 @@ cudaError_t launch_head_listed(const HeadRows &p, bool bf16, cudaStream_t s) {
                 : cudaLaunchKernelEx(&cfg, head_listed_kernel<__half>, p);
 }
 
-cudaError_t launch_head_join(const float *parts, long long n, long long part_stride, int nparts,
-                             const float *scale, float alpha, void *out, bool bf16, int sms,
-                             cudaStream_t s) {
-    long long ctas = (n / 8 + 255) / 256;
-    if (ctas > 16LL * sms) ctas = 16LL * sms;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config((unsigned)ctas, 1, 256, s, attr);
-    unsigned char *o = static_cast<unsigned char *>(out);
-    return bf16 ? cudaLaunchKernelEx(&cfg, head_join_kernel<__nv_bfloat16>, parts, n, part_stride,
-                                     nparts, scale, alpha, o)
-                : cudaLaunchKernelEx(&cfg, head_join_kernel<__half>, parts, n, part_stride, nparts,
-                                     scale, alpha, o);
-}
-
-cudaError_t launch_head_loss(float *rows, long long B, int reduction, const HeadInfo *info,
-                             float *loss_out, cudaStream_t s) {
+cudaError_t launch_head_loss(float *rows, long long B, int reduction, int mean_of_all,
+                             const HeadInfo *info, float *loss_out, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(1, 1, kTailThreads, s, attr);
-    return cudaLaunchKernelEx(&cfg, head_loss_kernel, rows, B, reduction, info, loss_out);
+    return cudaLaunchKernelEx(&cfg, head_loss_kernel, rows, B, reduction, mean_of_all, info,
+                              loss_out);
 }
 
 }  // namespace ce
