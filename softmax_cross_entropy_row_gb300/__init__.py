@@ -374,20 +374,20 @@ def _check_heads(rows, reduction, loss_out, grad_scale, **others) -> None:
     import torch
 
     n = rows if reduction == CE_REDUCE_NONE else 1
-    given = dict(others, loss_out=loss_out, grad_scale=grad_scale)
-    for name, t in given.items():
-        if t is not None and t.device.type != "cuda":
-            raise ValueError(f"{name} must be a CUDA tensor")
+    here = torch.cuda.current_device() if loss_out is not None and loss_out.is_cuda else -1
+    for name, t in (*others.items(), ("loss_out", loss_out), ("grad_scale", grad_scale)):
+        if t is not None and t.get_device() != here:
+            if not t.is_cuda or here < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} must be on the current CUDA device")
     if loss_out is None or loss_out.dtype != torch.float32 or loss_out.numel() < n \
             or not loss_out.is_contiguous():
         raise ValueError(f"loss_out must be a contiguous float32 tensor of at least {n} element(s)")
+    if here < 0:
+        raise ValueError("loss_out must be a CUDA tensor")
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != n
                                    or not grad_scale.is_contiguous()):
         raise ValueError(f"grad_scale must be a contiguous float32 tensor of {n} element(s)")
-    if len({t.device for t in given.values() if t is not None}) != 1:
-        raise ValueError("all tensors must be on one device")
-    if loss_out.device.index != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current CUDA device")
 
 
 def _check_projection(hidden, weight, dhidden_out, dweight_out) -> None:

@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // ------------------------------------------------------------- the parts
-// A warp per row of a split tile: its parts added in order.
+// A warp adds 128 columns of a row of a
+// split tile, its parts in order.
 template <int PROD, typename T>
 __global__ void __launch_bounds__(256)
     head_join_kernel(const __grid_constant__ HeadGemm p, unsigned char *out, int pairs) {
@@ -578,28 +579,24 @@ __global__ void __launch_bounds__(256)
         head_work(p, (HeadProduct)PROD, p.dynamic ? p.info->count : p.B, pairs);
     const int m_rows = PROD == kProdWeight ? p.C : work.rows;
     const float f0 = p.alpha * p.info->out;
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < work.rest * kTileM; i += gridDim.x * 8) {
-        const int r = i / kTileM, y = i % kTileM;
+    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < work.rest * kTileM * 2;
+         i += gridDim.x * 8) {
+        const int r = i / (kTileM * 2), y = i / 2 % kTileM, x = i % 2 * 128 + lane * 4;
         int mt, nt;
         head_tile(p, work, work.full + r, &mt, &nt);
-        const int row = mt * kTileM + y, col = nt * kTileN + lane * 8;
+        const int row = mt * kTileM + y, col = nt * kTileN + x;
         if (row >= m_rows || col >= p.D) continue;
         const float *src = p.parts + (size_t)r * work.splits * (kTileM * kTileN) +
-                           (size_t)y * kTileN + lane * 8;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+                           (size_t)y * kTileN + x;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int q = 0; q < work.splits; ++q) {
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(src));
-            const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + 4));
-            src += kTileM * kTileN;
-            v[0] += a.x;
-            v[1] += a.y;
-            v[2] += a.z;
-            v[3] += a.w;
-            v[4] += b.x;
-            v[5] += b.y;
-            v[6] += b.z;
-            v[7] += b.w;
+            const float4 a = __ldcg(
+                reinterpret_cast<const float4 *>(src + (size_t)q * (kTileM * kTileN)));
+            v.x += a.x;
+            v.y += a.y;
+            v.z += a.z;
+            v.w += a.w;
         }
         float f = f0;
         size_t at = row;
@@ -607,9 +604,8 @@ __global__ void __launch_bounds__(256)
             if (p.row_mul) f *= p.row_mul[(size_t)row * p.row_mul_stride];
             at = p.perm ? p.perm[p.first + row] : p.first + row;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        *reinterpret_cast<uint4 *>(out + (at * p.D + col) * 2) = E::pack(v);
+        *reinterpret_cast<uint2 *>(out + (at * p.D + col) * 2) =
+            make_uint2(E::pack2(f * v.x, f * v.y), E::pack2(f * v.z, f * v.w));
     }
 }
 

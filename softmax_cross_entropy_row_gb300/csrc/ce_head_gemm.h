@@ -82,14 +82,33 @@ struct HeadWork {
     int tiles_m, tiles_n, k_blocks;
     int full, rest, splits, units;
 };
-__host__ __device__ inline HeadWork head_work(const HeadGemm &p, HeadProduct prod, int count,
+
+#ifdef __CUDACC__
+// The parts (of at most 64, and kMaxParts per pair) that cost `rest` tiles of
+// k_blocks stages the least: a stage takes about 0.35 us, a part more, for its
+// 256 KB written and read and the launch that adds them up.  Every lane of the
+// warp tries two numbers and all get the answer.
+__device__ __forceinline__ int head_splits(int rest, int k_blocks, int pairs) {
+    const int lane = threadIdx.x & 31;
+    unsigned best = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = lane + 1 + 32 * i;
+        if (s > 1 && (rest * s > kMaxParts * pairs || k_blocks < 8 * s)) continue;
+        const unsigned rounds = (unsigned)(rest * s + pairs - 1) / (unsigned)pairs;
+        const unsigned ns = rounds * ((unsigned)(k_blocks + s - 1) / (unsigned)s) * 350u +
+                            (s > 1 ? 4000u + 80u * (unsigned)(rest * s) : 0u);
+        // in units of 64 ns, the number of parts below
+        best = min(best, (min(ns, 0xfffffffu) / 64u) << 6 | (unsigned)(s - 1));
+    }
+    return (int)(__reduce_min_sync(0xffffffffu, best) & 63u) + 1;
+}
+// Called by whole warps.
+__device__ __forceinline__ HeadWork head_work(const HeadGemm &p, HeadProduct prod, int count,
                                               int pairs) {
     HeadWork w;
     w.rows = p.rows;
-    if (p.dynamic) {
-        const int left = count - p.first;
-        w.rows = left < 0 ? 0 : left < p.rows ? left : p.rows;
-    }
+    if (p.dynamic) w.rows = min(max(count - p.first, 0), p.rows);
     const int m = prod == kProdWeight ? p.C : w.rows;
     const int n = prod == kProdLogits ? p.C : p.D;
     const int k = prod == kProdLogits ? p.D : prod == kProdHidden ? p.C : w.rows;
@@ -100,30 +119,18 @@ __host__ __device__ inline HeadWork head_work(const HeadGemm &p, HeadProduct pro
     w.full = tiles;
     w.rest = 0;
     w.splits = 1;
-    if (p.may_split) {
-        w.full = tiles / pairs * pairs;
-        w.rest = tiles - w.full;
-        // a stage takes about 0.35 us; a part more: its 256 KB written and read
-        // and, if there is any, a launch to add them up
-        long long best = 1LL << 60;
-        for (int s = 1; s <= 64 && w.rest > 0; ++s) {
-            if (s > 1 && (w.rest * s > kMaxParts * pairs || w.k_blocks / s < 8)) break;
-            const long long rounds = (w.rest * s + pairs - 1) / pairs;
-            const long long ns = rounds * ((w.k_blocks + s - 1) / s) * 350 +
-                                 (s > 1 ? 4000 + 80LL * w.rest * s : 0);
-            if (ns < best) {
-                best = ns;
-                w.splits = s;
-            }
-        }
-        if (w.splits == 1) {
-            w.full = tiles;
-            w.rest = 0;
+    if (p.may_split && tiles > 0) {
+        const int rest = tiles % pairs;
+        w.splits = rest > 0 ? head_splits(rest, w.k_blocks, pairs) : 1;
+        if (w.splits > 1) {
+            w.rest = rest;
+            w.full = tiles - rest;
         }
     }
     w.units = w.full + w.rest * w.splits;
     return w;
 }
+#endif
 
 // Tile t of the walk: groups of group_m tile rows, down the columns of each,
 // so that pairs working at the same time share operands in L2.

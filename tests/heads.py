@@ -12,7 +12,10 @@ rounded to the operands' type.  With u = finfo(type).eps / 2 the bounds count
               few ulp (2^-22) and the argument's rounding (|z| 2^-23):
               ds = (200 + C / 256) 2^-24 + 2^-21 + 2^-22 max|z|;
   kept p      two roundings to the operands' type, 2 u + u^2;
-  products    (terms / 16 + 16) 2^-23 of sum |a b|, then one rounding u.
+  products    (terms / 16 + 16) 2^-23 of sum |a b|, then one rounding u;
+  flushing    an exponential below 2^-126 counts as 0; the row's sum is at
+              least 2^-1/2 (its reference exponent is one of its classes',
+              rounded), so a p off by less than 2^-125.
 """
 
 import math
@@ -94,7 +97,7 @@ def cross_entropy(z, dz, targets, dtype, reduction, scale=None, ignore_index=-10
     y[r[valid], t[valid]] = 1.0
     u = unit(dtype)
     G = torch.where(keep[:, None], p - y, torch.zeros_like(p))
-    dG = kept * u * 1.01 * G.abs() + (2 * err[:, None]) * p
+    dG = kept * u * 1.01 * G.abs() + (2 * err[:, None]) * p + 2.0 ** -125
     if dtype == "f16":
         dG = dG + 2.0 ** -38 * f.abs().amax() / f.abs().clamp(min=1e-300)
     dG = torch.where(keep[:, None], dG, torch.zeros_like(dG))
@@ -122,8 +125,9 @@ def teacher_lists(B, C, K, seed, empty=0.0, ragged=False):
 
 
 def divergence(z, dz, idx, val, lse, T, dtype, reduction, scale=None, kept=2):
-    """The teacher's divergence; `kept` roundings of an unlisted gradient, one
-    of a listed one."""
+    """The teacher's divergence; `kept` roundings of a gradient.  (A listed one
+    is rounded once where it is kept; in bf16 its row's factor lies in the
+    hidden states, rounded with them, for the weights' gradient.)"""
     B, C = z.shape
     used = (idx >= 0) & (idx < C)
     bad = ((idx < -1) | (idx >= C)).any(1)
@@ -154,8 +158,9 @@ def divergence(z, dz, idx, val, lse, T, dtype, reduction, scale=None, kept=2):
     r = torch.arange(B, device="cuda")[:, None].expand_as(idx)
     listed[r[used], idx[used].long()] = True
     u = unit(dtype)
-    kept_p = torch.where(listed, u * G.abs(), kept * u * 1.01 * mass[:, None] * p)
-    dG = kept_p + mass[:, None] * p * (2 * err + eq)[:, None] + 2 * eq[:, None] * y
+    kept_p = kept * u * 1.01 * torch.where(listed, G.abs(), mass[:, None] * p)
+    dG = kept_p + mass[:, None] * (p * (2 * err + eq)[:, None] + 2.0 ** -125)
+    dG = dG + 2 * eq[:, None] * y
     if dtype == "f16":
         w = f.abs() * mass[:, None].clamp(min=1.0)
         dG = dG + 2.0 ** -38 * w.amax() / f.abs().clamp(min=1e-300)
