@@ -299,7 +299,7 @@ int run(const Call &c) {
     z.per_row = z.grad && bf16;
     z.ld = round_up(c.C, 64);
     z.tile_n = z.grad ? ce::kTileN : stats_tile(c.C, c.B, pairs);
-    z.tiles = (int)ceil_div(c.C, z.tile_n);
+    z.tiles = 2 * (int)ceil_div(c.C, z.tile_n);
     z.piece = z.grad ? rows_per_piece(c.B, c.D, c.C, c.dweight != nullptr)
                      : std::min(round_up(c.B, ce::kTileM),
                                 std::max<long long>(ce::kTileM, kPieceBytes / (8LL * z.tiles) /

@@ -7,9 +7,10 @@
 // One thread per CTA streams 64-wide slices of the operands into a ring of
 // six stages by TMA (each CTA of the pair loads its 128 rows of A and its
 // half of B, so a stage is 32 KB per SM and an operand byte is loaded once per
-// pair), one thread of the first CTA issues the matrix instructions, and four
-// warps per CTA drain the finished accumulator while the next tile's is being
-// formed (two accumulators of 256 columns: all of tensor memory).
+// pair), one thread of the first CTA issues the matrix instructions, and eight
+// warps per CTA (32 rows and half of the columns each) drain the finished
+// accumulator while the next tile's is being formed (two accumulators of 256
+// columns: all of tensor memory).
 //
 // The logits never leave the SM as logits: their epilogue turns a tile into
 // its rows' maximum and sum of exponentials (without the target's class), and,
@@ -27,9 +28,9 @@ constexpr int kStages = 6;
 constexpr int kCtaRows = kTileM / 2;               // rows of A and of B per CTA
 constexpr int kOperandBytes = kCtaRows * kTileK * 2;  // 16 KB
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 256;
-constexpr int kEpiWarp0 = 4;                       // warps 4..7: the epilogue
-constexpr int kEpiBufs = 2;
+constexpr int kEpiWarp0 = 4;                       // warps 4..11: the epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kEpiBufBytes = 32 * 128;             // 32 rows of 128 bytes
 constexpr uint32_t kTmemCols = 512;
 
@@ -42,7 +43,7 @@ struct Barriers {
 };
 
 constexpr int kSmemBytes =
-    kStages * kStageBytes + 4 * kEpiBufs * kEpiBufBytes + 1024 /* alignment */ + sizeof(Barriers);
+    kStages * kStageBytes + kEpiWarps * kEpiBufBytes + 1024 /* alignment */ + sizeof(Barriers);
 
 // Work unit u: a tile, and the part [k0, k1) of its contraction.
 struct Unit {
@@ -83,26 +84,22 @@ __device__ __forceinline__ float pick(const float (&v)[32], int j) {
     return x;
 }
 
-// The epilogue's staging boxes of one warp: two, so that one is filled while
-// the other is on its way out.
+// The epilogue's staging box of one warp.  open() waits until the box's last
+// store has read it (it has had the time of a TMEM load and the arithmetic).
 struct Stager {
-    unsigned char *base;
-    int n;
-    __device__ __forceinline__ unsigned char *open() {
-        // the group that used this box two commits ago has been read
-        if ((threadIdx.x & 31) == 0) bulk_wait_read<kEpiBufs - 1>();
+    unsigned char *box;
+    __device__ __forceinline__ void open() {
+        if ((threadIdx.x & 31) == 0) bulk_wait_read<0>();
         __syncwarp();
-        return base + n * kEpiBufBytes;
     }
     template <typename F>
     __device__ __forceinline__ void close(F issue) {
         fence_proxy_async();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) {
-            issue(base + n * kEpiBufBytes);
+            issue(box);
             bulk_commit();
         }
-        n ^= 1;
     }
 };
 
@@ -193,9 +190,9 @@ __device__ __forceinline__ void exponentials(const float (&v)[32], float exp_sca
 // the tile's sum of exponentials S 2^M.
 template <typename E, bool KEEP>
 __device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &w, const Unit &u,
-                                             uint32_t acc, int m0, Stager &st) {
-    const int n0 = u.nt * p.tile_n;
-    const int cols = min(p.tile_n, p.C - n0);
+                                             uint32_t acc, int m0, int half, Stager &st) {
+    const int n0 = u.nt * p.tile_n + half * (p.tile_n / 2);
+    const int cols = min(p.tile_n / 2, p.C - n0);
     const LogitRow r = logit_row(p, w, m0, n0, cols);
     float v[32];
     float m = -INFINITY;
@@ -216,17 +213,20 @@ __device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &
     const float M = m == -INFINITY ? 0.f : m * p.exp_scale - p.shift;
     unsigned long long sum = 0ull;
     for (int c0 = 0; c0 < cols; c0 += 64) {
-        unsigned char *box = KEEP ? st.open() : nullptr;
         load_logits(v, acc, c0, cols, r);
-        exponentials<E, KEEP>(v, p.exp_scale, M, sum, box, 0, !r.counts);
-        load_logits(v, acc, c0 + 32, cols, r);
-        exponentials<E, KEEP>(v, p.exp_scale, M, sum, box, 4, !r.counts);
+        if (KEEP) st.open();
+        exponentials<E, KEEP>(v, p.exp_scale, M, sum, st.box, 0, !r.counts);
+        if (KEEP || c0 + 32 < cols) {
+            load_logits(v, acc, c0 + 32, cols, r);
+            exponentials<E, KEEP>(v, p.exp_scale, M, sum, st.box, 4, !r.counts);
+        }
         if (KEEP) st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
     }
     if (r.counts) {
         float a, b;
         f2_unpack(sum, a, b);
-        p.stats[(size_t)u.nt * p.rows + r.row] = make_float2(m == -INFINITY ? -INFINITY : M, a + b);
+        p.stats[(size_t)(2 * u.nt + half) * p.rows + r.row] =
+            make_float2(m == -INFINITY ? -INFINITY : M, a + b);
     }
 }
 
@@ -234,42 +234,42 @@ __device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &
 // the tile's largest exponent m and its sum of exponentials S 2^ref.
 template <typename E>
 __device__ __forceinline__ void epi_ref(const HeadGemm &p, const HeadWork &w, const Unit &u,
-                                        uint32_t acc, int m0, Stager &st) {
-    const int n0 = u.nt * kTileN;
-    const int cols = min(kTileN, p.C - n0);
+                                        uint32_t acc, int m0, int half, Stager &st) {
+    const int n0 = u.nt * kTileN + half * kStatN;
+    const int cols = min(kStatN, p.C - n0);
     const LogitRow r = logit_row(p, w, m0, n0, cols);
     const float M = r.counts ? p.ref[r.row] : 0.f;
     float v[32];
     float m = -INFINITY;
     unsigned long long sum = 0ull;
     for (int c0 = 0; c0 < cols; c0 += 64) {
-        unsigned char *box = st.open();
         load_logits(v, acc, c0, cols, r);
         m = fmaxf(m, max32(v));
-        exponentials<E, true>(v, p.exp_scale, M, sum, box, 0, !r.counts);
+        st.open();
+        exponentials<E, true>(v, p.exp_scale, M, sum, st.box, 0, !r.counts);
         load_logits(v, acc, c0 + 32, cols, r);
         m = fmaxf(m, max32(v));
-        exponentials<E, true>(v, p.exp_scale, M, sum, box, 4, !r.counts);
+        exponentials<E, true>(v, p.exp_scale, M, sum, st.box, 4, !r.counts);
         st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
     }
     if (r.counts) {
         float a, b;
         f2_unpack(sum, a, b);
-        p.stats[(size_t)u.nt * p.rows + r.row] = make_float2(m * p.exp_scale, a + b);
+        p.stats[(size_t)(2 * u.nt + half) * p.rows + r.row] = make_float2(m * p.exp_scale, a + b);
     }
 }
 
 // A part of a tile in fp32 to its place among the parts.
 __device__ __forceinline__ void epi_part(const HeadGemm &p, const Unit &u, uint32_t acc, int row0,
-                                         Stager &st) {
+                                         int half, Stager &st) {
     const int lane = threadIdx.x & 31;
-    float *at = p.parts + (size_t)u.part * (kTileM * kTileN) + (size_t)(row0 + lane) * kTileN;
+    float *at = p.parts + (size_t)u.part * (kTileM * kTileN) + (size_t)(row0 + lane) * kTileN +
+                half * kStatN;
     float v[32];
-    if (lane == 0) bulk_wait_read<0>();  // a store of the tile before may still read the box
-    __syncwarp();
+    st.open();  // a store of the tile before may still read the box
+    unsigned char *box = st.box;
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
-        unsigned char *box = st.base;
+    for (int c = 0; c < kStatN; c += 32) {
         tmem_ld32(acc + c, v);
         tmem_wait_ld(v);
 #pragma unroll
@@ -285,7 +285,7 @@ __device__ __forceinline__ void epi_part(const HeadGemm &p, const Unit &u, uint3
 // place in the call's batch.
 template <typename E>
 __device__ __forceinline__ void epi_hidden(const HeadGemm &p, const HeadWork &w, const Unit &u,
-                                           uint32_t acc, int m0, float f, Stager &st) {
+                                           uint32_t acc, int m0, int half, float f, Stager &st) {
     const int lane = threadIdx.x & 31;
     const int row = m0 + lane;
     const bool counts = row < w.rows;
@@ -296,10 +296,11 @@ __device__ __forceinline__ void epi_hidden(const HeadGemm &p, const HeadWork &w,
         at = p.dhidden + (size_t)b * p.D * 2;
     }
     float v[32];
-    const int cols = min(kTileN, p.D - u.nt * kTileN);
+    const int n0 = u.nt * kTileN + half * kStatN;
+    const int cols = min(kStatN, p.D - n0);
+    unsigned char *box = st.box;
 #pragma unroll 1
     for (int c0 = 0; c0 < cols; c0 += 64) {
-        unsigned char *box = st.base;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             tmem_ld32(acc + c0 + 32 * h, v);
@@ -312,58 +313,60 @@ __device__ __forceinline__ void epi_hidden(const HeadGemm &p, const HeadWork &w,
                 stage16(box, lane, 4 * h + q, E::pack(x));
             }
         }
-        unstage(box, at ? at + (size_t)(u.nt * kTileN + c0) * 2 : nullptr, (cols - c0) * 2);
+        unstage(box, at ? at + (size_t)(n0 + c0) * 2 : nullptr, (cols - c0) * 2);
     }
 }
 
 // The weights' gradient in 16 bits (`zero`: no row counts).
 template <typename E>
 __device__ __forceinline__ void epi_weight(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                           float f, bool zero, Stager &st) {
+                                           int half, float f, bool zero, Stager &st) {
     const int lane = threadIdx.x & 31;
     float v[32];
-    const int cols = min(kTileN, p.D - u.nt * kTileN);
+    const int n0 = u.nt * kTileN + half * kStatN;
+    const int cols = min(kStatN, p.D - n0);
 #pragma unroll 1
     for (int c0 = 0; c0 < cols; c0 += 64) {
-        unsigned char *box = st.open();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             tmem_ld32(acc + c0 + 32 * h, v);
             tmem_wait_ld(v);
+            if (h == 0) st.open();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : f * v[8 * q + i];
-                stage16(box, lane, 4 * h + q, E::pack(x));
+                stage16(st.box, lane, 4 * h + q, E::pack(x));
             }
         }
-        st.close([&](const void *src) { tma_store(&p.out, src, u.nt * kTileN + c0, m0); });
+        st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
     }
 }
 
 // The weights' gradient in fp32, over several pieces of the rows.
 template <bool ADD>
 __device__ __forceinline__ void epi_f32(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                        bool zero, Stager &st) {
+                                        int half, bool zero, Stager &st) {
     const int lane = threadIdx.x & 31;
     float v[32];
-    const int cols = min(kTileN, p.D - u.nt * kTileN);
+    const int n0 = u.nt * kTileN + half * kStatN;
+    const int cols = min(kStatN, p.D - n0);
 #pragma unroll 1
     for (int c = 0; c < cols; c += 32) {
-        unsigned char *box = st.open();
         tmem_ld32(acc + c, v);
         tmem_wait_ld(v);
+        st.open();
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const float x[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-            stage16(box, lane, q, zero ? make_uint4(0u, 0u, 0u, 0u) : Elem<float>::pack(x));
+            stage16(st.box, lane, q, zero ? make_uint4(0u, 0u, 0u, 0u) : Elem<float>::pack(x));
         }
         st.close([&](const void *src) {
             if (ADD)
-                tma_add(&p.out, src, u.nt * kTileN + c, m0);
+                tma_add(&p.out, src, n0 + c, m0);
             else
-                tma_store(&p.out, src, u.nt * kTileN + c, m0);
+                tma_store(&p.out, src, n0 + c, m0);
         });
     }
 }
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // 1024-byte aligned (a swizzle atom), at the same offset in both CTAs
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *boxes = smem + kStages * kStageBytes;
-    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + 4 * kEpiBufs * kEpiBufBytes);
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpiWarps * kEpiBufBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.acc_full[i], 1);
-            mbar_init(&bar.acc_empty[i], 8);  // four warps of each CTA
+            mbar_init(&bar.acc_empty[i], 2 * kEpiWarps);  // of both CTAs
         }
         fence_mbar_init();
         prefetch_map(&p.a);
@@ -513,11 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (ok) commit_pair(&bar.acc_full[ab]);
         }
     } else if (warp >= kEpiWarp0) {
-        // ---- the epilogue: warp w drains lanes 32 (w mod 4) ..
+        // ---- the epilogue: warp w drains lanes 32 (w mod 4) .., half of the
+        // columns
         const int quad = warp & 3;
+        const int half = (warp - kEpiWarp0) >> 2;
         Stager st;
-        st.base = boxes + (warp - kEpiWarp0) * kEpiBufs * kEpiBufBytes;
-        st.n = 0;
+        st.box = boxes + (warp - kEpiWarp0) * kEpiBufBytes;
         float f = 1.f;
         if constexpr (EPI == kEpiOut) f = p.alpha * p.info->out;
         // a whole contraction may lie between two finished accumulators
@@ -533,23 +537,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int ab = it & 1;
             if (!wait_or_fail(p, &bar.acc_full[ab], (it >> 1) & 1, acc_limit)) break;
             tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN;
+            const uint32_t acc =
+                tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN + half * (p.tile_n / 2);
             const int row0 = rank * kCtaRows + quad * 32;
             const int m0 = u.mt * kTileM + row0;
             if (m0 < rows) {
-                if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, st);
-                if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, st);
-                if constexpr (EPI == kEpiRef) epi_ref<E>(p, work, u, acc, m0, st);
+                if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, half, st);
+                if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, half, st);
+                if constexpr (EPI == kEpiRef) epi_ref<E>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiOut) {
                     if (u.part >= 0)
-                        epi_part(p, u, acc, row0, st);
+                        epi_part(p, u, acc, row0, half, st);
                     else if constexpr (PROD == kProdHidden)
-                        epi_hidden<E>(p, work, u, acc, m0, f, st);
+                        epi_hidden<E>(p, work, u, acc, m0, half, f, st);
                     else
-                        epi_weight<E>(p, u, acc, m0, f, zero, st);
+                        epi_weight<E>(p, u, acc, m0, half, f, zero, st);
                 }
-                if constexpr (EPI == kEpiF32) epi_f32<false>(p, u, acc, m0, zero, st);
-                if constexpr (EPI == kEpiAdd) epi_f32<true>(p, u, acc, m0, zero, st);
+                if constexpr (EPI == kEpiF32) epi_f32<false>(p, u, acc, m0, half, zero, st);
+                if constexpr (EPI == kEpiAdd) epi_f32<true>(p, u, acc, m0, half, zero, st);
             }
             tc_fence_before();
             __syncwarp();

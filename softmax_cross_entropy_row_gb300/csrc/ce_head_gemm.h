@@ -16,6 +16,9 @@ namespace ce {
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kTileK = 64;
+// Columns of a tile that one warp drains; the logits' statistics are per half
+// tile.
+constexpr int kStatN = kTileN / 2;
 
 // What the launches of one call share on the device.
 struct HeadInfo {
@@ -58,7 +61,7 @@ struct HeadGemm {
     float shift;                   // kEpiKeep: the exponentials are kept times 2^shift
     const int32_t *targets;        // [B], nullptr: none
     const int *perm;               // the counting rows' places, nullptr: all in order
-    float2 *stats;                 // [column tiles][rows]
+    float2 *stats;                 // [half column tiles][rows]
     float *zt;                     // [rows] target logits (kEpiStats, kEpiKeep)
     const float *ref;              // [rows] reference exponents
     const int *only_if;            // nullptr, or: nothing to do unless set

@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadRows p) {
 }
 
 // ------------------------------------------------------ kept exponentials
-// A warp per 256 columns of a row (one tile, one factor), eight of them in
-// flight.
+// A warp per 256 columns of a row (two half tiles, a factor for each half of the
+// warp), eight of them in flight.
 constexpr int kScaleTiles = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long groups = (p.tiles + kScaleTiles - 1) / kScaleTiles;
+    const int tiles = p.tiles / 2;
+    const long long groups = (tiles + kScaleTiles - 1) / kScaleTiles;
     const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (i >= groups * piece_rows(p)) return;
     const int row = (int)(i / groups);
@@ -400,9 +401,8 @@ __global__ void __launch_bounds__(256) head_scale_kernel(HeadRows p) {
     for (int k = 0; k < kScaleTiles; ++k) {
         const long long c = (long long)(j0 + k) * 256 + lane * 8;
         if (c < p.ld) x[k] = *reinterpret_cast<const uint4 *>(base + c * 2);
-        f[k] = j0 + k < p.tiles
-                   ? ex2(__ldcg(&p.stats[(size_t)(j0 + k) * p.rows + row].x) - h.M) * h.mul
-                   : 0.f;
+        const int j = 2 * (j0 + k) + (lane >> 4);
+        f[k] = j < p.tiles ? ex2(__ldcg(&p.stats[(size_t)j * p.rows + row].x) - h.M) * h.mul : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kScaleTiles; ++k) {
@@ -577,7 +577,7 @@ cudaError_t launch_head_rows(const HeadRows &p, bool bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_head_scale(const HeadRows &p, bool bf16, cudaStream_t s) {
-    const long long groups = (p.tiles + kScaleTiles - 1) / kScaleTiles;
+    const long long groups = (p.tiles / 2 + kScaleTiles - 1) / kScaleTiles;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config((unsigned)((groups * p.rows + 7) / 8), 1, 256, s, attr);
     return bf16 ? cudaLaunchKernelEx(&cfg, head_scale_kernel<__nv_bfloat16>, p)

@@ -67,7 +67,7 @@ struct HeadTeacher {
 struct HeadRows {
     int B, C, D;
     int dynamic, first, rows;  // as in HeadGemm
-    int tiles;                 // column tiles of the statistics
+    int tiles;                 // half column tiles (statistics per row)
     const float2 *stats;       // [tiles][rows]
     const float *zt;           // [rows]
     float *ref;                // [rows], or nullptr: an exponent per tile
