@@ -133,9 +133,16 @@ long long rows_per_piece(long long B, long long D, long long C, bool dweight) {
     return std::min(round_up(B, ce::kTileM), std::max<long long>(r, ce::kTileM));
 }
 
-// Width of the loss alone's column tiles for rows that fill one tile at most
-// (the weights are then read at the memory's rate and the matrix instructions
-// have time): the one that spreads the classes evenly over the pairs.
+// Classes of a tile where the weights are read at the memory's rate: as many
+// as spread evenly over the pairs (a tile's two halves are copied and computed
+// in groups of 8 classes).
+int score_tile(long long C, int pairs) {
+    const long long rounds = ceil_div(C, (long long)ce::kTileM * pairs);
+    return (int)std::min<long long>(ce::kTileM, round_up(ceil_div(C, rounds * pairs), 16));
+}
+
+// The same for the loss alone of a batch of one tile's rows: the width of its
+// column tiles.
 int stats_tile(long long C, long long rows, int pairs) {
     int best = ce::kTileN;
     if (rows > ce::kTileM) return best;
@@ -240,8 +247,8 @@ struct Parts {
 
 struct Sizes {
     long long piece, pieces, ld;  // rows per piece, pieces, exponentials' row
-    int tile_n, tiles;
-    bool grad, per_row, weight_f32;
+    int tile_m, tile_n, tiles;
+    bool grad, per_row, weight_f32, score;
 };
 
 Parts carve(Carver &w, const Call &c, const Sizes &z, int pairs) {
@@ -298,8 +305,12 @@ int run(const Call &c) {
     z.grad = c.dhidden || c.dweight;
     z.per_row = z.grad && bf16;
     z.ld = round_up(c.C, 64);
-    z.tile_n = z.grad ? ce::kTileN : stats_tile(c.C, c.B, pairs);
-    z.tiles = 2 * (int)ceil_div(c.C, z.tile_n);
+    z.score = !z.grad && c.B <= ce::kScoreRows;
+    z.tile_m = z.score ? score_tile(c.C, pairs) : ce::kTileM;
+    z.tile_n = z.score ? (int)round_up(c.B, 32) : z.grad ? ce::kTileN
+                                                         : stats_tile(c.C, c.B, pairs);
+    z.tiles = z.score ? ce::kScoreStats * (int)ceil_div(c.C, z.tile_m)
+                      : 2 * (int)ceil_div(c.C, z.tile_n);
     z.piece = z.grad ? rows_per_piece(c.B, c.D, c.C, c.dweight != nullptr)
                      : std::min(round_up(c.B, ce::kTileM),
                                 std::max<long long>(ce::kTileM, kPieceBytes / (8LL * z.tiles) /
@@ -397,6 +408,7 @@ int run(const Call &c) {
         g.rows = (int)rows;
         g.C = (int)c.C;
         g.D = (int)c.D;
+        g.tile_m = z.tile_m;
         g.tile_n = z.tile_n;
         g.alpha = 1.f;
         g.exp_scale = exp_scale;
@@ -412,8 +424,13 @@ int run(const Call &c) {
         g.parts = ws.parts;
         g.clear_failed = i == 0;
         g.clear_rescue = z.per_row;
-        CE_TRY(tensor_map(&g.a, c.dtype, h, rows, c.D, c.D, ce::kTileM / 2));
-        CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, z.tile_n / 2));
+        if (z.score) {
+            CE_TRY(tensor_map(&g.a, c.dtype, c.weight, c.C, c.D, c.D, z.tile_m / 2));
+            CE_TRY(tensor_map(&g.b, c.dtype, h, rows, c.D, c.D, z.tile_n / 2));
+        } else {
+            CE_TRY(tensor_map(&g.a, c.dtype, h, rows, c.D, c.D, ce::kTileM / 2));
+            CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, z.tile_n / 2));
+        }
         if (z.grad) {
             CE_TRY(tensor_map(&g.packed, c.dtype, hp, padded, c.D, c.D, ce::kTileM / 2));
             CE_TRY(tensor_map(&g.out, c.dtype, ws.exps, padded, z.ld, z.ld, 32));
@@ -423,7 +440,8 @@ int run(const Call &c) {
         g.group_m = 16;
         const ce::HeadEpilogue epi =
             !z.grad ? ce::kEpiStats : z.per_row ? ce::kEpiRef : ce::kEpiKeep;
-        CE_CUDA(ce::launch_head_gemm(g, ce::kProdLogits, epi, bf16, pairs, s));
+        CE_CUDA(ce::launch_head_gemm(g, z.score ? ce::kProdScore : ce::kProdLogits, epi, bf16,
+                                     pairs, s));
 
         ce::HeadRows r = {};
         r.B = (int)c.B;

@@ -1,6 +1,7 @@
 // The three matrix products of a vocabulary projection and its loss, on the
 // tensor cores (tcgen05) of CTA pairs:
 //   logits  Z = H W^T        H [rows][D], W [C][D]: both operands lie along K
+//   score   Z^T = W H^T      the same for few rows
 //   hidden  dH = E W         E [rows][C] along K, W along N
 //   weight  dW = E^T H       E along M, H along N
 // A persistent kernel: each pair of CTAs takes tiles of 256 x 256 in turn.
@@ -24,10 +25,14 @@
 namespace ce {
 namespace {
 
-constexpr int kStages = 6;
 constexpr int kCtaRows = kTileM / 2;               // rows of A and of B per CTA
 constexpr int kOperandBytes = kCtaRows * kTileK * 2;  // 16 KB
-constexpr int kStageBytes = 2 * kOperandBytes;
+// The ring: six stages of 16 + 16 KB; with few rows as B eleven of 16 + 4 KB.
+constexpr int kMaxStages = 11;
+__host__ __device__ constexpr int stages_of(int prod) { return prod == kProdScore ? 11 : 6; }
+__host__ __device__ constexpr int stage_bytes(int prod) {
+    return kOperandBytes + (prod == kProdScore ? kScoreRows / 2 * kTileK * 2 : kOperandBytes);
+}
 constexpr int kEpiWarp0 = 4;                       // warps 4..11: the epilogue
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -35,15 +40,18 @@ constexpr int kEpiBufBytes = 32 * 128;             // 32 rows of 128 bytes
 constexpr uint32_t kTmemCols = 512;
 
 struct Barriers {
-    uint64_t full[kStages];
-    uint64_t empty[kStages];
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint32_t tmem;
 };
 
-constexpr int kSmemBytes =
-    kStages * kStageBytes + kEpiWarps * kEpiBufBytes + 1024 /* alignment */ + sizeof(Barriers);
+__host__ __device__ constexpr int box_bytes(int prod) { return prod == kProdScore ? 0 : kEpiWarps * kEpiBufBytes; }
+constexpr int smem_bytes(int prod) {
+    return stages_of(prod) * stage_bytes(prod) + box_bytes(prod) + 1024 /* alignment */ +
+           (int)sizeof(Barriers);
+}
 
 // Work unit u: a tile, and the part [k0, k1) of its contraction.
 struct Unit {
@@ -230,6 +238,46 @@ __device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &
     }
 }
 
+// Few rows: this lane's class against 32 rows of the batch.  A row's maximum
+// and sum over the warp's classes: one reduction instruction per row for the
+// maximum, a transposing tree of shuffles (lane i ends with row i) for the sum.
+__device__ __forceinline__ void epi_score(const HeadGemm &p, const Unit &u, uint32_t acc,
+                                          int class0, int classes, int stat, int row0) {
+    const int lane = threadIdx.x & 31;
+    float v[32], e[32];
+    tmem_ld32(acc + row0, v);
+    tmem_wait_ld(v);
+    const int row = row0 + lane;
+    int target = -1;
+    if (p.targets != nullptr && row < p.rows) target = __ldg(p.targets + p.first + row);
+    float mine = -INFINITY;  // row `row`'s maximum
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (lane >= classes) v[i] = -INFINITY;
+        const int t = __shfl_sync(0xffffffffu, target, i);
+        if (t >= 0 && t == class0 + lane && lane < classes && row0 + i < p.rows) {
+            p.zt[row0 + i] = v[i];
+            v[i] = -INFINITY;
+        }
+        const float m = warp_max(v[i]);
+        if (i == lane) mine = m;
+        const float M = m == -INFINITY ? 0.f : m * p.exp_scale;
+        e[i] = ex2(fmaf(v[i], p.exp_scale, -M));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float give = up ? e[i] : e[i + o], keep = up ? e[i + o] : e[i];
+            e[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    if (row < p.rows)
+        p.stats[(size_t)(u.mt * kScoreStats + stat) * p.rows + row] =
+            make_float2(mine == -INFINITY ? -INFINITY : mine * p.exp_scale, e[0]);
+}
+
 // Exponentials relative to the row's given exponent, in one pass: (m, S) with
 // the tile's largest exponent m and its sum of exponentials S 2^ref.
 template <typename E>
@@ -386,13 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     head_gemm_kernel(const __grid_constant__ HeadGemm p) {
     using E = Elem<T>;
     constexpr bool kAMn = PROD == kProdWeight;
-    constexpr bool kBMn = PROD != kProdLogits;
+    constexpr bool kBMn = PROD == kProdHidden || PROD == kProdWeight;
+    constexpr int kStages = stages_of(PROD);
+    constexpr int kStageBytes = stage_bytes(PROD);
     constexpr bool kBf16 = E::kNegInfWord == Elem<__nv_bfloat16>::kNegInfWord;
     extern __shared__ unsigned char smem_raw[];
     // 1024-byte aligned (a swizzle atom), at the same offset in both CTAs
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *boxes = smem + kStages * kStageBytes;
-    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpiWarps * kEpiBufBytes);
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + box_bytes(PROD));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -435,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const CUtensorMap *map_a = PROD == kProdLogits && packed ? &p.packed : &p.a;
     const CUtensorMap *map_b = PROD == kProdWeight && packed ? &p.packed : &p.b;
     const int half_n = p.tile_n / 2;  // rows of B per CTA
+    const int half_m = p.tile_m / 2;  // rows of A per CTA (the rest of its 128 do not matter)
 
     if (warp == 0 && lane == 0) {
         // ---- the producer: this CTA's halves of A and B
@@ -443,12 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         bool ok = true;
         for (int w = pair; ok && w < units; w += pairs) {
             const Unit u = unit_of(p, work, w);
-            const int m0 = u.mt * kTileM + rank * kCtaRows;
+            const int m0 = u.mt * p.tile_m + rank * half_m;
             const int n0 = u.nt * p.tile_n + rank * half_n;
             for (int k = u.k0; k < u.k1; ++k) {
                 if (!(ok = wait_or_fail(p, &bar.empty[s], ph ^ 1u))) break;
                 if (rank == 0)
-                    mbar_arrive_expect_tx(&bar.full[s], 2 * (kOperandBytes + half_n * kTileK * 2));
+                    mbar_arrive_expect_tx(&bar.full[s], 2 * (half_m + half_n) * kTileK * 2);
                 const uint32_t fb = mapa(&bar.full[s], 0);
                 unsigned char *da = smem + s * kStageBytes;
                 unsigned char *db = da + kOperandBytes;
@@ -541,7 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN + half * (p.tile_n / 2);
             const int row0 = rank * kCtaRows + quad * 32;
             const int m0 = u.mt * kTileM + row0;
-            if (m0 < rows) {
+            if constexpr (PROD == kProdScore) {
+                // this warp's classes, and every second 32 rows of the batch
+                const int class0 = u.mt * p.tile_m + rank * half_m + quad * 32;
+                const int classes = min(half_m - quad * 32, p.C - class0);
+                for (int r0 = half * 32; r0 < work.rows; r0 += 64)
+                    epi_score(p, u, tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN, class0,
+                              classes, rank * 4 + quad, r0);
+            } else if (m0 < rows) {
                 if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiRef) epi_ref<E>(p, work, u, acc, m0, half, st);
@@ -648,16 +706,18 @@ cudaLaunchConfig_t config(unsigned ctas, unsigned threads, size_t smem, cudaStre
 template <int PROD, int EPI, typename T>
 cudaError_t launch_t(const HeadGemm &p, int pairs, cudaStream_t s) {
     const void *f = reinterpret_cast<const void *>(head_gemm_kernel<PROD, EPI, T>);
-    cudaError_t e = ensure_smem_attr(f, kSmemBytes);
+    cudaError_t e = ensure_smem_attr(f, smem_bytes(PROD));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config((unsigned)(2 * pairs), kThreads, kSmemBytes, s, attr);
+    cudaLaunchConfig_t cfg = config((unsigned)(2 * pairs), kThreads, smem_bytes(PROD), s, attr);
     return cudaLaunchKernelEx(&cfg, head_gemm_kernel<PROD, EPI, T>, p);
 }
 
 template <typename T>
 cudaError_t launch_of(const HeadGemm &p, HeadProduct prod, HeadEpilogue epi, int pairs,
                       cudaStream_t s) {
+    if (prod == kProdScore && epi == kEpiStats)
+        return launch_t<kProdScore, kEpiStats, T>(p, pairs, s);
     if (prod == kProdLogits && epi == kEpiStats)
         return launch_t<kProdLogits, kEpiStats, T>(p, pairs, s);
     if (prod == kProdLogits && epi == kEpiKeep)

@@ -41,7 +41,12 @@ enum HeadEpilogue {
 
 // Which way the operands lie: the logits (both rows along K), the gradient of
 // the hidden states (weights along N) and of the weights (both along M, N).
-enum HeadProduct { kProdLogits = 0, kProdHidden = 1, kProdWeight = 2 };
+// For few rows the logits are formed the other way round, Z^T = W H^T (score):
+// the classes then fill the tensor cores' 256 rows and the memory's whole rate
+// goes into the weights' copies.
+enum HeadProduct { kProdLogits = 0, kProdHidden = 1, kProdWeight = 2, kProdScore = 3 };
+constexpr int kScoreRows = 64;  // rows of the batch, at most
+constexpr int kScoreStats = 8;  // statistics per tile: 32 classes each
 
 struct HeadGemm {
     CUtensorMap a, b, out;
@@ -52,6 +57,7 @@ struct HeadGemm {
     int first, rows;               // rows of this piece, at most
     int C, D;
     int tile_n;                    // kEpiStats: width of a tile (else kTileN)
+    int tile_m;                    // score: classes of a tile, in two halves (else kTileM)
     int group_m;                   // tile rows that are walked together
     int may_split;                 // the last tiles' contraction may be split
     float *parts;                  // fp32 tiles of the split parts (kMaxParts a pair)
@@ -112,10 +118,11 @@ __device__ __forceinline__ HeadWork head_work(const HeadGemm &p, HeadProduct pro
     HeadWork w;
     w.rows = p.rows;
     if (p.dynamic) w.rows = min(max(count - p.first, 0), p.rows);
-    const int m = prod == kProdWeight ? p.C : w.rows;
-    const int n = prod == kProdLogits ? p.C : p.D;
-    const int k = prod == kProdLogits ? p.D : prod == kProdHidden ? p.C : w.rows;
-    w.tiles_m = (m + kTileM - 1) / kTileM;
+    const int m = prod == kProdWeight || prod == kProdScore ? p.C : w.rows;
+    const int n = prod == kProdLogits ? p.C : prod == kProdScore ? w.rows : p.D;
+    const int k = prod == kProdLogits || prod == kProdScore ? p.D
+                  : prod == kProdHidden ? p.C : w.rows;
+    w.tiles_m = (m + p.tile_m - 1) / p.tile_m;
     w.tiles_n = (n + p.tile_n - 1) / p.tile_n;
     w.k_blocks = (k + kTileK - 1) / kTileK;
     const int tiles = w.tiles_m * w.tiles_n;

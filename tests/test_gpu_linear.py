@@ -83,6 +83,21 @@ def test_linear_reductions(reduction, grads, dtype):
     check_linear(h, w, t, dtype, reduction, scale, grads=grads)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B", [1, 2, 31, 32, 33, 64, 65, 128, 257])
+@pytest.mark.parametrize("D,C", [(8, 1), (64, 250), (200, 5003), (264, 40000)])
+def test_loss_alone(B, D, C, dtype):
+    """Few rows (classes as the tiles' rows, up to 64 rows of the batch), one
+    tile's and more."""
+    t = some_targets(B, C, B, ignored=0.1)
+    t[B // 2] = C - 1
+    h, w = heads.projection(B, D, C, dtype, B + C, raised=t)
+    check_linear(h, w, t, dtype, NONE, grads="none")
+    check_linear(h, w, t, dtype, MEAN, grads="none")
+    idx, val = heads.teacher_lists(B, C, 4, B)
+    check_linear_distill(h, w, idx, val, dtype, reduction=NONE, grads="none")
+
+
 def test_linear_upstream_gradients_of_any_size():
     """f16 keeps the rows' gradients relative to the largest upstream one."""
     B, D, C = 90, 64, 333
