@@ -372,7 +372,7 @@ int ce_linear_fwd_bwd(const void *hidden, const void *weight, const int32_t *tar
  *                probability 0.
  *   teacher_lse  device [B] fp32, or NULL.
  *   K            1 .. 1024 (CE_ERR_SHAPE).
- *   temperature  positive and finite (CE_ERR_TEMPERATURE).
+ *   temperature  positive and finite, like its reciprocal (CE_ERR_TEMPERATURE).
  *   reduction, grad_scale, loss_out: as for ce_fwd_bwd_ex.
  *   grad_out     device [B][C] in `dtype`, or NULL: the loss alone.
  *

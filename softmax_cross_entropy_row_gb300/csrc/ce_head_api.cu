@@ -38,14 +38,27 @@ std::mutex g_mu;  // held over a whole call: its launches use the workspace
 std::map<std::tuple<int, uintptr_t, unsigned long long>, Buffer> g_buffers;
 std::vector<std::pair<int, unsigned char *>> g_outgrown;  // of captures
 
+// While it lives, this thread may allocate, free and wait although some stream
+// of its is being captured (none of it becomes part of a capture).
+struct Relaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 int workspace(int dev, cudaStream_t s, size_t need, unsigned char **out) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     cudaError_t e = cudaStreamGetCaptureInfo(s, &cs, &id);
     if (e != cudaSuccess) return ce::host_cuda_fail(e);
     if (cs != cudaStreamCaptureStatusActive) id = 0;
-    Buffer &b = g_buffers[{dev, reinterpret_cast<uintptr_t>(s), id}];
+    // the per-thread default stream has one handle for all threads
+    static thread_local char thread_key;
+    const uintptr_t key = s == cudaStreamPerThread ? reinterpret_cast<uintptr_t>(&thread_key)
+                                                   : reinterpret_cast<uintptr_t>(s);
+    Buffer &b = g_buffers[{dev, key, id}];
     if (b.bytes < need) {
+        const Relaxed relaxed;
         if (b.base) {
             if (id) {
                 g_outgrown.push_back({dev, b.base});
@@ -116,6 +129,9 @@ int tensor_map(CUtensorMap *map, int dtype, const void *base, long long rows, lo
 
 // ------------------------------------------------------------------ plans
 
+// The reciprocal has to be a number too.
+bool temperature_ok(float t) { return t > 0.f && isfinite(t) && isfinite(ce::kLog2e / t); }
+
 constexpr size_t kTicketOffset = 128;          // within the workspace's first 256 bytes
 constexpr long long kMaxK = 1024;             // places of a teacher's list
 constexpr long long kPieceBytes = 1LL << 30;  // kept exponentials, see rows_per_piece
@@ -158,6 +174,10 @@ int stats_tile(long long C, long long rows, int pairs) {
     return best;
 }
 
+// Whether a contraction of at most k may be split (head_splits: parts of at
+// least 8 stages).
+int can_split(long long k) { return ceil_div(k, ce::kTileK) >= 16; }
+
 struct Call {
     const void *hidden, *weight;
     const int32_t *targets;  // cross-entropy
@@ -194,7 +214,7 @@ int check(const Call &c) {
     if (ceil_div(c.C, ce::kTileN) * ceil_div(std::max(c.B, c.D), ce::kTileM) * 32 > 0x7fffffffLL ||
         ceil_div(c.B, ce::kTileM) * ceil_div(c.D, ce::kTileM) * 32 > 0x7fffffffLL)
         return CE_ERR_SHAPE;
-    if (teacher && !(c.temperature > 0.f && isfinite(c.temperature))) return CE_ERR_TEMPERATURE;
+    if (teacher && !temperature_ok(c.temperature)) return CE_ERR_TEMPERATURE;
     const auto off = [](const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a; };
     const uintptr_t te = c.teacher_dtype == CE_F32 ? 4 : 2;
     if (off(c.hidden, 16) || off(c.weight, 16) || off(c.dhidden, 16) || off(c.dweight, 16) ||
@@ -422,6 +442,7 @@ int run(const Call &c) {
         g.rescue = &ws.info->rescue;
         g.err = err;
         g.parts = ws.parts;
+        g.dhidden = static_cast<unsigned char *>(c.dhidden);
         g.clear_failed = i == 0;
         g.clear_rescue = z.per_row;
         if (z.score) {
@@ -498,12 +519,12 @@ int run(const Call &c) {
             CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, padded, z.ld, z.ld, ce::kTileM / 2));
             CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileK));
             g.group_m = 8;
-            g.may_split = 1;
+            g.may_split = can_split(c.C);
             g.row_mul = z.per_row ? &ws.row->mul : nullptr;
             g.row_mul_stride = sizeof(ce::HeadRow) / sizeof(float);
-            g.dhidden = static_cast<unsigned char *>(c.dhidden);
             CE_CUDA(ce::launch_head_gemm(g, ce::kProdHidden, ce::kEpiOut, bf16, pairs, s));
-            CE_CUDA(ce::launch_head_join(g, ce::kProdHidden, c.dhidden, bf16, pairs, s));
+            if (g.may_split)
+                CE_CUDA(ce::launch_head_join(g, ce::kProdHidden, c.dhidden, bf16, pairs, s));
         }
         if (c.dweight) {
             if (z.per_row) CE_CUDA(ce::launch_head_scale_hidden(r, s));
@@ -520,13 +541,13 @@ int run(const Call &c) {
             else
                 CE_TRY(tensor_map(&g.out, c.dtype, c.dweight, c.C, c.D, c.D, 32));
             g.group_m = 8;
-            g.may_split = !z.weight_f32;
+            g.may_split = !z.weight_f32 && can_split(rows);
             CE_CUDA(ce::launch_head_gemm(g, ce::kProdWeight,
                                          !z.weight_f32 ? ce::kEpiOut
                                          : i == 0      ? ce::kEpiF32
                                                        : ce::kEpiAdd,
                                          bf16, pairs, s));
-            if (!z.weight_f32)
+            if (g.may_split)
                 CE_CUDA(ce::launch_head_join(g, ce::kProdWeight, c.dweight, bf16, pairs, s));
         }
     }
@@ -564,7 +585,7 @@ int check(const DistillCall &c) {
     if (c.B < 1 || c.C < 1 || c.K < 1 || c.K > kMaxK || c.B > 0x7fffffffLL || c.C > 0x7fffffffLL ||
         (unsigned long long)c.B * (unsigned long long)c.C > (1ull << 61) / es)
         return CE_ERR_SHAPE;
-    if (!(c.temperature > 0.f && isfinite(c.temperature))) return CE_ERR_TEMPERATURE;
+    if (!temperature_ok(c.temperature)) return CE_ERR_TEMPERATURE;
     const auto off = [](const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a; };
     if (off(c.logits, es) || off(c.grad, es) || off(c.idx, 4) || off(c.val, te) || off(c.lse, 4) ||
         off(c.scale, 4) || off(c.loss, 4))

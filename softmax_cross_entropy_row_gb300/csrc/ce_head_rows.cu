@@ -52,56 +52,59 @@ __global__ void __launch_bounds__(kPrepThreads) head_prep_kernel(HeadPrep p) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // each thread has a run of rows: their places follow from one scan
-    const long long run = (p.B + kPrepThreads - 1) / kPrepThreads;
-    const long long b0 = min(p.B, run * threadIdx.x), b1 = min(p.B, b0 + run);
-    auto counts_at = [&](long long b) {
-        return p.targets ? __ldg(p.targets + b) != p.ignore_index : p.mass[b] != 0.f;
-    };
+    // each warp has a run of rows, 32 at a time: first their count, then, with
+    // the counts of the warps before it, their places
+    const long long run = (p.B + 1023) / 1024 * 32;
+    const long long b0 = min(p.B, run * warp), b1 = min(p.B, b0 + run);
     int n = 0, bad = 0;
     float norm = 0.f;
-    for (long long b = b0; b < b1; ++b) {
-        const bool c = counts_at(b);
-        n += c;
-        if (p.targets && c) {
+#pragma unroll 4
+    for (long long b = b0 + lane; b < b1; b += 32) {
+        bool c;
+        float w = p.scale_per_row ? fabsf(__ldg(p.scale + b)) : 1.f;
+        if (p.targets) {
             const int t = __ldg(p.targets + b);
-            bad += t < 0 || t >= p.C;
+            c = t != p.ignore_index;
+            bad += c && (t < 0 || t >= p.C);
+        } else {
+            const float mass = p.mass[b];
+            c = mass != 0.f;
+            w *= fmaxf(fabsf(mass), 1.f);
         }
-        if (c) {
-            float w = p.scale_per_row ? fabsf(__ldg(p.scale + b)) : 1.f;
-            if (!p.targets) w *= fmaxf(fabsf(p.mass[b]), 1.f);
-            norm = fmaxf(norm, w);
-        }
+        n += c;
+        if (c) norm = fmaxf(norm, w);
     }
-    int before = n;  // rows of this warp's threads up to this one
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-    }
+    n = __reduce_add_sync(0xffffffffu, n);
     norm = warp_max(norm);
-    if (lane == 31) {
-        counts[warp] = before;
+    if (lane == 0) {
+        counts[warp] = n;
         norms[warp] = norm;
     }
     if (p.perm && bad) atomicAdd(&p.err[kErrBadTarget], bad);
     __syncthreads();
-    int base = 0, total = 0;
-    norm = 0.f;
-    for (int i = 0; i < 32; ++i) {
-        if (i < warp) base += counts[i];
-        total += counts[i];
-        norm = fmaxf(norm, norms[i]);
-    }
+    const int before = lane < warp ? counts[lane] : 0;
+    int at = __reduce_add_sync(0xffffffffu, before);
+    const int total = __reduce_add_sync(0xffffffffu, counts[lane]);
+    norm = warp_max(norms[lane]);
     if (p.perm) {
-        int at = base + before - n;
-        for (long long b = b0; b < b1; ++b) {
-            if (counts_at(b)) {
-                p.pos[b] = at;
-                p.perm[at++] = (int)b;
-            } else {
+#pragma unroll 4
+        for (long long i = b0; i < b1; i += 32) {
+            const long long b = i + lane;
+            bool c = false;
+            float mass = 0.f;
+            if (b < b1) {
+                if (!p.targets) mass = p.mass[b];
+                c = p.targets ? __ldg(p.targets + b) != p.ignore_index : mass != 0.f;
+            }
+            const unsigned those = __ballot_sync(0xffffffffu, c);
+            const int place = at + __popc(those & ((1u << lane) - 1u));
+            at += __popc(those);
+            if (c) {
+                p.pos[b] = place;
+                p.perm[place] = (int)b;
+            } else if (b < b1) {
                 p.pos[b] = -1;
-                p.loss[b] = !p.targets && signbit(p.mass[b]) ? NAN : 0.f;
+                p.loss[b] = !p.targets && signbit(mass) ? NAN : 0.f;
             }
         }
     }
@@ -557,18 +560,13 @@ namespace {
 template <typename T>
 cudaError_t rows_of(const HeadRows &p, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
-    // enough CTAs for the rows there are: 32 rows each in a large batch, one
-    // each where there are few
+    // eight rows per CTA (32 threads each), or one where that leaves SMs idle
     if (p.rows <= 256) {
         cudaLaunchConfig_t cfg = config((unsigned)p.rows, 1, 256, s, attr);
         return cudaLaunchKernelEx(&cfg, head_rows_kernel<1, T>, p);
     }
-    if (p.rows <= 2048) {
-        cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 7) / 8), 1, 256, s, attr);
-        return cudaLaunchKernelEx(&cfg, head_rows_kernel<8, T>, p);
-    }
-    cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 31) / 32), 1, 256, s, attr);
-    return cudaLaunchKernelEx(&cfg, head_rows_kernel<32, T>, p);
+    cudaLaunchConfig_t cfg = config((unsigned)((p.rows + 7) / 8), 1, 256, s, attr);
+    return cudaLaunchKernelEx(&cfg, head_rows_kernel<8, T>, p);
 }
 }  // namespace
 

@@ -126,6 +126,27 @@ def test_repeated_and_bad_classes(B, C, K):
     assert ce.ce_get_device_errors() == (3, 0)
 
 
+@pytest.mark.parametrize("B,C,K", [(400, 3, 500), (10, 3, 1000), (400, 1000, 900), (1, 5, 4)])
+def test_lists_longer_than_the_row(B, C, K):
+    g = torch.Generator("cuda").manual_seed(6)
+    idx = torch.randint(-1, C, (B, K), generator=g, device="cuda", dtype=torch.int32)
+    val = torch.randn(B, K, generator=g, device="cuda") * 3
+    for dtype in ("f32", "f16"):
+        check_distill(student(B, C, dtype, 6), idx, val, dtype, reduction=NONE)
+
+
+@pytest.mark.parametrize("B,C", KERNELS)
+def test_cold_and_hot(B, C):
+    """Temperatures at which the softmax is one class, and uniform."""
+    idx, val = heads.teacher_lists(B, C, 5, 8)
+    z = student(B, C, "f32", 8, idx, val)
+    for T in (1e-3, 1e4):
+        check_distill(z, idx, val, "f32", T=T, reduction=NONE)
+    loss, grad = torch.empty(B, device="cuda"), torch.empty_like(z)
+    ce.ce_distill_fwd_bwd(z, idx, val, loss, grad, temperature=1e-30, reduction=NONE)
+    assert not torch.isnan(grad).any() and not torch.isnan(loss).any()
+
+
 @pytest.mark.parametrize("B,C", KERNELS)
 def test_values_at_the_types_ends(B, C):
     """Student: -inf for classes ruled out, whole rows of the type's lowest

@@ -297,6 +297,29 @@ def test_graphs_replayed_at_the_same_time():
     check_linear(*cases[0][:3], "bf16")
 
 
+def test_a_growing_workspace_beside_a_capture():
+    """While one stream is being captured, a call on another one may need a
+    larger workspace: the capture goes on."""
+    t = some_targets(300, 900, 5)
+    h, w = heads.projection(300, 64, 900, "bf16", 5, raised=t)
+    t2 = some_targets(900, 20000, 6)
+    h2, w2 = heads.projection(900, 128, 20000, "bf16", 6, raised=t2)
+    side = torch.cuda.Stream()
+    small, large = outputs(h, w, MEAN), outputs(h2, w2, MEAN)
+    torch.cuda.synchronize()
+    ce.ce_linear_fwd_bwd(h, w, t, *small, stream=side)
+    g = torch.cuda.CUDAGraph()
+    out = outputs(h, w, MEAN)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        ce.ce_linear_fwd_bwd(h, w, t, *out)
+        ce.ce_linear_fwd_bwd(h2, w2, t2, *large, stream=side)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, small))
+    assert all(torch.equal(a, b) for a, b in zip(large, check_linear(h2, w2, t2, "bf16")))
+
+
 def test_gradients_against_differences():
     """Central differences of the loss along a direction.  The quotient is off
     by at most r^3 d^2 / 3 (the third derivative of a row's log-sum-exp along a

@@ -69,6 +69,7 @@ def test_teacher_refusals(lib, call):
             (dict(K=1025), SHAPE), (dict(K=-1), SHAPE), (dict(tdtype=3), DTYPE),
             (dict(T=0.0), TEMPERATURE), (dict(T=-1.0), TEMPERATURE),
             (dict(T=math.inf), TEMPERATURE), (dict(T=math.nan), TEMPERATURE),
+            (dict(T=2.0 ** -149), TEMPERATURE),
             (dict(idx=3 * M + 2), ALIGN), (dict(val=7 * M + 2), ALIGN),
             (dict(lse=8 * M + 2), ALIGN), (dict(val=7 * M + 1, tdtype=ce.CE_F16), ALIGN),
             (dict(loss=3 * M + 4), OVERLAP), (dict(loss=7 * M + 4), OVERLAP),
