@@ -59,11 +59,22 @@ __device__ __forceinline__ MS join(MS a, MS b, float scale) {
     return {m, a.s * ex2((a.m - m) * scale) + b.s * ex2((b.m - m) * scale)};
 }
 
-// The teacher's list of row b, by one warp: classes and log-probabilities to
-// shared memory (unused and bad places: class -1), and whether a class was out
-// of range.  Returns the mass.
-__device__ __forceinline__ float read_list(const DistillParams &p, long long b, int *idx,
-                                           float *lq, int *bad) {
+// What a row's list comes to.
+struct ListSums {
+    float mass;    // sum q
+    float negent;  // sum q log q
+    bool bad;      // a class was out of range
+};
+
+// The teacher's list of row b, by one warp: classes and probabilities to shared
+// memory (unused and bad places: class -1, probability 0), and, if `z` is
+// given, the row's logits there (loaded while the probabilities are formed).
+// One exponential per place: with x_k = (t_k - m) / T,
+//   q_k = e^x_k / s, sum q log q = (sum e^x x) / s - log s     (s = sum e^x), or
+//   q_k = e^(x_k - ref)                                        (lse given).
+template <typename E>
+__device__ __forceinline__ ListSums read_list(const DistillParams &p, long long b, int *cls,
+                                              float *prob, float *z, const unsigned char *row) {
     const int lane = threadIdx.x & 31;
     const long long i0 = b * p.K;
     const float inv_t = 1.f / p.temperature;
@@ -79,32 +90,50 @@ __device__ __forceinline__ float read_list(const DistillParams &p, long long b, 
             c = -1;
         }
         if (c < 0) t = -INFINITY;
-        idx[k] = c;
-        lq[k] = t;
+        cls[k] = c;
+        prob[k] = t;
         m = fmaxf(m, t);
+        // a NaN is not the maximum, but the place has to count
+        if (t != t) m = fmaxf(m, -3.402823466e38f);
+    }
+    if (z != nullptr) {
+#pragma unroll 4
+        for (int k = lane; k < p.list_words; k += 32)
+            z[k] = cls[k] >= 0 ? E::load_global(row + (size_t)cls[k] * E::kBytes) : 0.f;
     }
     m = warp_max(m);
-    float ref;
-    if (p.lse != nullptr) {
-        ref = __ldg(p.lse + b) - m * inv_t;
+    ListSums r = {0.f, 0.f, (bool)__any_sync(0xffffffffu, wrong)};
+    if (m == -INFINITY) {  // no place has a probability
+        for (int k = lane; k < p.list_words; k += 32) prob[k] = 0.f;
+    } else if (p.lse != nullptr) {
+        const float ref = __ldg(p.lse + b) - m * inv_t;
+        for (int k = lane; k < p.list_words; k += 32) {
+            const float x = (prob[k] - m) * inv_t - ref;
+            const float q = expf(x);
+            if (q != 0.f) r.negent += q * x;
+            r.mass += q;
+            prob[k] = q;
+        }
+        r.mass = warp_sum(r.mass);
+        r.negent = warp_sum(r.negent);
     } else {
-        float s = 0.f;
-        for (int k = lane; k < p.K; k += 32)
-            if (idx[k] >= 0) s += expf((lq[k] - m) * inv_t);
-        ref = logf(warp_sum(s));
+        float s = 0.f, sx = 0.f;
+        for (int k = lane; k < p.list_words; k += 32) {
+            const float x = (prob[k] - m) * inv_t;
+            const float e = expf(x);
+            if (e != 0.f) sx += e * x;
+            s += e;
+            prob[k] = e;
+        }
+        s = warp_sum(s);
+        sx = warp_sum(sx);
+        const float inv = 1.f / s;
+        for (int k = lane; k < p.list_words; k += 32) prob[k] *= inv;
+        r.mass = s == s ? 1.f : s;
+        r.negent = sx * inv - logf(s);
     }
-    float q = 0.f;
-    for (int k = lane; k < p.K; k += 32) {
-        if (idx[k] < 0) continue;
-        // m = -inf: no place has a probability
-        const float v = m == -INFINITY ? -INFINITY : (lq[k] - m) * inv_t - ref;
-        lq[k] = v;
-        q += expf(v);
-    }
-    q = warp_sum(q);
-    *bad = __any_sync(0xffffffffu, wrong);
     __syncwarp();
-    return q;
+    return r;
 }
 
 // What one warp keeps of a row's list, in shared memory.
@@ -134,36 +163,33 @@ __device__ __forceinline__ int find(const int *key, int bits, int c) {
     return (int)at;
 }
 
-// cls and prob (log-probabilities on entry) with the places of a class added
-// up, by one warp; returns sum_k q_k log q_k.  A hash table finds out whether
-// any class is listed twice.  Only then the later places' probabilities are
-// added to the first's, as multiples of 2^-40, whose sums do not depend on the
-// order of the additions.
-__device__ __forceinline__ float merge_list(const List &l, int words, int bits) {
+__device__ __forceinline__ void clear_table(const List &l, int bits) {
+    for (int i = threadIdx.x & 31; i < (1 << bits); i += 32) l.key[i] = -1;
+    __syncwarp();
+}
+
+// cls and prob with the places of a class added up, by one warp (the table has
+// been cleared).  A hash table finds out whether any class is listed twice.
+// Only then the later places' probabilities are added to the first's, as
+// multiples of 2^-40, whose sums do not depend on the order of the additions
+// (z is formed anew then).  Returns whether that was so.
+__device__ __forceinline__ bool merge_list(const List &l, int words, int bits) {
     const int lane = threadIdx.x & 31;
     const int size = 1 << bits;
-    for (int i = lane; i < size; i += 32) l.key[i] = -1;
-    __syncwarp();
     bool twice = false;
-    float h = 0.f;
     for (int k = lane; k < words; k += 32) {
         const int c = l.cls[k];
-        float q = 0.f;
-        if (c >= 0) {
-            const float v = l.prob[k];
-            q = expf(v);
-            if (q != 0.f) h += q * v;
-            unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
-            for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
-                const int was = atomicCAS(&l.key[at], -1, c);
-                twice |= was == c;
-                if (was == -1 || was == c) break;
-                at = (at + 1) & (size - 1);
-            }
+        if (c < 0) continue;
+        unsigned at = ((unsigned)c * 2654435761u) >> (32 - bits);
+        for (int n = 0; n < size; ++n) {  // at most half full: ends earlier
+            const int was = atomicCAS(&l.key[at], -1, c);
+            twice |= was == c;
+            if (was == -1 || was == c) break;
+            at = (at + 1) & (size - 1);
         }
-        l.prob[k] = q;
     }
-    if (__any_sync(0xffffffffu, twice)) {
+    twice = __any_sync(0xffffffffu, twice);
+    if (twice) {
         constexpr float kUnit = 1099511627776.f;  // 2^40
         for (int i = lane; i < size; i += 32) l.first[i] = words;
         for (int k = lane; k < words; k += 32) l.acc[k] = 0ull;
@@ -184,7 +210,28 @@ __device__ __forceinline__ float merge_list(const List &l, int words, int bits) 
             l.prob[k] += (float)((double)l.acc[k] * (1.0 / (double)kUnit));
         __syncwarp();
     }
-    return warp_sum(h);
+    return twice;
+}
+
+// A row's list complete: read, merged, with the row's logits in z.
+template <typename E>
+__device__ __forceinline__ ListSums take_list(const DistillParams &p, long long b, const List &l,
+                                              int bits, const unsigned char *row) {
+    const int words = p.list_words;
+    clear_table(l, bits);
+    const ListSums r = read_list<E>(p, b, l.cls, l.prob, l.z, row);
+    if (merge_list(l, words, bits))  // z lies in the sums' place
+        for (int k = threadIdx.x & 31; k < words; k += 32)
+            l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * E::kBytes) : 0.f;
+    __syncwarp();
+    return r;
+}
+
+// The row of this warp after next on its way to L2: its list.
+__device__ __forceinline__ void prefetch_list(const DistillParams &p, long long b) {
+    const int vs = p.val_dtype == 0 ? 4 : 2;
+    prefetch_l2(p.idx + b * p.K, 4LL * p.K);
+    prefetch_l2(static_cast<const unsigned char *>(p.val) + b * p.K * vs, (long long)vs * p.K);
 }
 
 // A row's place in memory: nh elements up to a 16-byte boundary, nvec whole
@@ -311,7 +358,7 @@ __device__ __forceinline__ void put_vector(unsigned char *g, const uint4 &v, boo
 
 // CTAs per SM the registers are set for: a thread keeps V vectors of its row.
 constexpr int min_ctas(int g, int v, bool loop) {
-    return loop ? 2 : g == 128 ? 4 : g == 32 && v == 8 ? 3 : 2;
+    return loop ? 2 : g == 128 ? 4 : g == 32 && v < 16 ? (v == 8 ? 3 : 4) : 2;
 }
 
 template <typename T, int G, int V, bool LOOP>
@@ -325,7 +372,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
     __shared__ MS part[2][WARPS * GROUPS];
     __shared__ float lpart[2][WARPS * GROUPS];
     __shared__ float4 mine[2];  // this CTA's share, read by the cluster
-    __shared__ float masses[2];
+    __shared__ float masses[2], negents[2];
     __shared__ int bads[2];
     __shared__ int tail_flag;
     __shared__ float2 tail_scratch[kTailWarps];
@@ -367,29 +414,20 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
         int *idx = reinterpret_cast<int *>(lists) + buf * 2 * p.list_words;
         float *lq = reinterpret_cast<float *>(idx + p.list_words);
         List l = {};
-        float warp_mass = 0.f, warp_negent = 0.f;
-        int warp_bad = 0;
+        ListSums sums = {0.f, 0.f, false};
         if constexpr (G == 32) {
             l = list_at(lists + group * list_bytes(p.list_words, bits), p.list_words, bits);
-            // the next row of this warp on its way to L2
             if (b + step < p.B) {
-                const long long i1 = (b + step) * p.K;
-                const int vs = p.val_dtype == 0 ? 4 : 2;
                 prefetch_l2(row + (size_t)(step * p.C) * ES, p.C * ES);
-                prefetch_l2(p.idx + i1, 4LL * p.K);
-                prefetch_l2(static_cast<const unsigned char *>(p.val) + i1 * vs, (long long)vs * p.K);
+                prefetch_list(p, b + step);
             }
-            warp_mass = read_list(p, b, l.cls, l.prob, &warp_bad);
-            warp_negent = merge_list(l, p.list_words, bits);
-#pragma unroll 2
-            for (int k = lane; k < p.list_words; k += 32)
-                l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
+            sums = take_list<E>(p, b, l, bits, row);
         } else if (warp == 0) {
-            int bad;
-            const float q = read_list(p, b, idx, lq, &bad);
+            const ListSums r = read_list<E>(p, b, idx, lq, nullptr, row);
             if (lane == 0) {
-                masses[buf] = q;
-                bads[buf] = bad;
+                masses[buf] = r.mass;
+                negents[buf] = r.negent;
+                bads[buf] = r.bad;
             }
         }
 
@@ -426,7 +464,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             __syncwarp();
         }
         const float m = a.m, S = a.s;
-        const float mass = G == 32 ? warp_mass : masses[buf];
+        const float mass = G == 32 ? sums.mass : masses[buf];
         const float f = row_grad_factor(p, scalar, b) * p.temperature;
         const float inv = 1.f / S;
 
@@ -477,9 +515,9 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             }
             cross = warp_sum(cross);
             if (lane == 0) {
-                float loss = (warp_negent - kLn2 * cross) * p.temperature * p.temperature;
+                float loss = (sums.negent - kLn2 * cross) * p.temperature * p.temperature;
                 if (mass == 0.f) loss = 0.f;
-                if (warp_bad) {
+                if (sums.bad) {
                     loss = NAN;
                     atomicAdd(&p.err[kErrBadTarget], 1);
                 }
@@ -488,16 +526,15 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
             __syncwarp();
             continue;
         }
-        float loss = 0.f;
+        float cross = 0.f;
         for (int k = t; k < p.K; k += G) {
             const int c = idx[k];
             if (c < 0) continue;
             const bool here = c >= sp.e0 && c < sp.e1;
             if (!here && rank != 0) continue;
             const float lp2 = (E::load_global(row + (size_t)c * ES) - m) * scale - log2S;
-            const float v = lq[k];
-            const float q = expf(v);
-            if (q != 0.f) loss += q * (v - kLn2 * lp2);
+            const float q = lq[k];
+            if (q != 0.f) cross += q * lp2;
             if (!writes_grad(p) || !here) continue;
             float all = 0.f;
             bool mine_first = true;
@@ -508,7 +545,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
                 for (int i = 0; i < 4; ++i) {
                     if (oc[i] != c) continue;
                     if (j + i < k) mine_first = false;
-                    all += expf(lq[j + i]);
+                    all += lq[j + i];
                 }
             }
             if (mine_first)
@@ -516,13 +553,13 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
                          mass == 0.f ? 0.f : (mass * ex2(lp2) - all) * f);
         }
         if (rank == 0) {
-            loss = warp_sum(loss);
-            if (lane == 0) lpart[buf][warp] = loss;
+            cross = warp_sum(cross);
+            if (lane == 0) lpart[buf][warp] = cross;
             __syncthreads();
-            loss = lpart[buf][0];
-            for (int i = 1; i < WARPS; ++i) loss += lpart[buf][i];
+            cross = lpart[buf][0];
+            for (int i = 1; i < WARPS; ++i) cross += lpart[buf][i];
             if (t == 0) {
-                loss *= p.temperature * p.temperature;
+                float loss = (negents[buf] - kLn2 * cross) * p.temperature * p.temperature;
                 if (mass == 0.f) loss = 0.f;
                 if (bads[buf]) {
                     loss = NAN;
@@ -667,16 +704,18 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
         for (long long b = blockIdx.x + (long long)j * gridDim.x; b < p.B;
              b += (long long)LW * gridDim.x, ph ^= 1u) {
             const unsigned char *row = p.logits + (size_t)(b * p.C) * ES;
-            int bad;
-            const float mass = read_list(p, b, l.cls, l.prob, &bad);
+            const long long next = b + (long long)LW * gridDim.x;
+            if (next < p.B) prefetch_list(p, next);
+            clear_table(l, rs.table_bits);
+            const ListSums sums = read_list<E>(p, b, l.cls, l.prob, l.z, row);
+            const float mass = sums.mass;
             if (lane == 0) {
                 masses[j] = mass;
                 mbar_arrive(&list_full[j]);  // the reducing warps need the mass alone
             }
-            const float negent = merge_list(l, words, rs.table_bits);
-#pragma unroll 4
-            for (int k = lane; k < words; k += 32)
-                l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
+            if (merge_list(l, words, rs.table_bits))
+                for (int k = lane; k < words; k += 32)
+                    l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
             if (!__all_sync(0xffffffffu, mbar_wait(&row_done[j], ph))) {
                 if (lane == 0) fail();
                 break;
@@ -697,9 +736,9 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             }
             cross = warp_sum(cross);
             if (lane == 0) {
-                float loss = (negent - kLn2 * cross) * p.temperature * p.temperature;
+                float loss = (sums.negent - kLn2 * cross) * p.temperature * p.temperature;
                 if (mass == 0.f) loss = 0.f;
-                if (bad) {
+                if (sums.bad) {
                     loss = NAN;
                     atomicAdd(&p.err[kErrBadTarget], 1);
                 }
@@ -851,6 +890,8 @@ const void *kernel_of(const DistillPlan &pl) {
     if (pl.ring_threads == 512)
         return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, true>);
     if (pl.loop) return reinterpret_cast<const void *>(distill_kernel<T, 512, 8, true>);
+    if (pl.group == 32 && pl.vecs == 4)
+        return reinterpret_cast<const void *>(distill_kernel<T, 32, 4, false>);
     if (pl.group == 32 && pl.vecs == 8)
         return reinterpret_cast<const void *>(distill_kernel<T, 32, 8, false>);
     if (pl.group == 32) return reinterpret_cast<const void *>(distill_kernel<T, 32, 16, false>);
@@ -905,6 +946,7 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
     if (row <= 8192 && 8 * list_bytes(words, r.table_bits) <= 65536) {
         r.group = 32;
         if (row <= 4096) r.vecs = 8;
+        if (row <= 2048) r.vecs = 4;
     } else {
         // few rows: up to 8 CTAs each, as long as every SM then has one
         while (r.cluster < 8 && B * r.cluster * 2 <= sms && row / r.cluster > 16384) r.cluster *= 2;
