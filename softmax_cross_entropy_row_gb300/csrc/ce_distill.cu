@@ -585,13 +585,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) disti
 // stores, and writes the listed classes and the loss, without their waiting
 // for it (done by one of the reducing warps, it held the others up at the next
 // row's barrier: 268 us on 8192 x 32000 bf16).
-// Vectors per thread and chunk: chunks of 8, 16, 16 and 32 KB.
-__host__ __device__ constexpr int ring_vecs(int nt, bool resident) {
-    return nt == 512 && resident ? 2 : 4;
-}
-__host__ __device__ constexpr int chunk_bytes(int nt, bool resident) {
-    return nt * 16 * ring_vecs(nt, resident);
-}
+constexpr int kRingVecs = 4;  // per thread and chunk: chunks of 8, 16 and 32 KB
+__host__ __device__ constexpr int chunk_bytes(int nt) { return nt * 16 * kRingVecs; }
 constexpr int kMaxSlots = 16;
 
 struct RingShape {
@@ -609,8 +604,8 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
     distill_ring_kernel(DistillParams p, RingShape rs) {
     using E = Elem<T>;
     constexpr int ES = E::kBytes;
-    constexpr int V = ring_vecs(NT, RESIDENT);
-    constexpr int CH = chunk_bytes(NT, RESIDENT);
+    constexpr int V = kRingVecs;
+    constexpr int CH = chunk_bytes(NT);
     constexpr int VC = CH / 16;
     constexpr int NW = NT / 32;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -766,7 +761,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             const float lz = lc >= 0 ? E::load_global(row + lc * ES) : -INFINITY;
             MS a = {lz, lz == -INFINITY ? 0.f : lz == lz ? 1.f : lz};
             const int nvec = (int)sp.v1;
-            // chunk at vector v (all of it there, or the row's last) to registers
+            // this thread's vectors of the chunk at vector v
             auto fetch = [&](int slot, int v, uint4 (&x)[V]) {
                 const unsigned char *src = ring + slot * CH + t * 16;
                 if (v + VC <= nvec) {
@@ -781,6 +776,16 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                                                 E::kNegInfWord);
                 }
             };
+            // whether a chunk is more than half there: all its rounds at once
+            auto mostly = [&](int v) { return v + VC / 2 < nvec; };
+            // vector k of a row's last chunk, one round at a time (a 98 KB row is
+            // three chunks and a little)
+            auto fetch_one = [&](int slot, int v, int k, uint4 (&x)[1]) {
+                x[0] = v + k * NT + t < nvec
+                           ? lds128(ring + slot * CH + (k * NT + t) * 16)
+                           : make_uint4(E::kNegInfWord, E::kNegInfWord, E::kNegInfWord,
+                                        E::kNegInfWord);
+            };
             auto release = [&](int slot) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[slot]);
@@ -792,10 +797,19 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             const int s0 = s;
             for (int v = 0; v < nvec; v += VC) {
                 if (wait(&full[s], ph)) {
-                    uint4 x[V];
-                    fetch(s, v, x);
-                    if (!RESIDENT || !grads) release(s);
-                    add_vectors<E, V>(a, x, scale);
+                    if (mostly(v)) {
+                        uint4 x[V];
+                        fetch(s, v, x);
+                        if (!RESIDENT || !grads) release(s);
+                        add_vectors<E, V>(a, x, scale);
+                    } else {
+                        for (int k = 0; v + k * NT < nvec; ++k) {
+                            uint4 x[1];
+                            fetch_one(s, v, k, x);
+                            add_vectors<E, 1>(a, x, scale);
+                        }
+                        if (!RESIDENT || !grads) release(s);
+                    }
                 }
                 if (++s == S) {
                     s = 0;
@@ -829,7 +843,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                 const Exponent ex(m, scale);
                 for (int v = 0; v < nvec; v += VC, gt += CH) {
                     if (!RESIDENT) wait(&full[r], ph);
-                    if (ok) {
+                    if (ok && mostly(v)) {
                         uint4 x[V];
                         fetch(r, v, x);
                         release(r);
@@ -849,6 +863,18 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                                 if (v + k * NT + t < nvec)
                                     put_vector<E>(gt + k * NT * 16, x[k], p.grad_vec_ok);
                         }
+                    } else if (ok) {
+                        for (int k = 0; k < V && v + k * NT < nvec; ++k) {
+                            uint4 x[1];
+                            fetch_one(r, v, k, x);
+                            if (zero)
+                                x[0] = make_uint4(0u, 0u, 0u, 0u);
+                            else
+                                to_gradients<E, 1>(x, ex, fs);
+                            if (v + k * NT + t < nvec)
+                                put_vector<E>(gt + k * NT * 16, x[0], p.grad_vec_ok);
+                        }
+                        release(r);
                     }
                     if (++r == S) {
                         r = 0;
@@ -881,14 +907,12 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
 // two passes.
 template <typename T>
 const void *kernel_of(const DistillPlan &pl) {
-    if (pl.ring_threads && !pl.resident)
-        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, false>);
     if (pl.ring_threads == 128)
         return reinterpret_cast<const void *>(distill_ring_kernel<T, 128, true>);
     if (pl.ring_threads == 256)
         return reinterpret_cast<const void *>(distill_ring_kernel<T, 256, true>);
     if (pl.ring_threads == 512)
-        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, true>);
+        return reinterpret_cast<const void *>(distill_ring_kernel<T, 512, false>);
     if (pl.loop) return reinterpret_cast<const void *>(distill_kernel<T, 512, 8, true>);
     if (pl.group == 32 && pl.vecs == 4)
         return reinterpret_cast<const void *>(distill_kernel<T, 32, 4, false>);
@@ -959,26 +983,23 @@ cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, 
         }
     }
     if (r.group != 32 && B > sms) {
-        // The ring of the smallest CTA that holds the row, of 512 threads only
-        // where it holds 1.7 rows; longer rows are streamed twice.  Measured
-        // (K = 64, bf16 and fp32, fraction of the copy bandwidth): 31 KB rows
-        // 0.77 in 128 threads (0.66-0.73 in 256), 62 KB rows 0.86 in 256 (0.70-
-        // 0.77 in 512), 94 KB fp32 rows 0.90 in 512 threads, 128 KB bf16 rows
-        // 0.98 streamed twice (0.89 resident in 512), 196 KB fp32 rows 0.94
-        // streamed twice (0.91 resident).
+        // The ring of the smallest CTA (128 threads, four per SM, or 256, two)
+        // that holds the row; longer rows are streamed twice through one of 512
+        // threads.  Measured (K = 64, bf16 and fp32, fraction of the copy
+        // bandwidth): 31 KB rows 0.77 in 128 threads (0.66-0.73 in 256), 62 KB
+        // rows 0.86-0.88 in 256 (0.70-0.77 in 512), 94 KB rows 0.86-0.88 in 256; a
+        // resident ring of 512 threads was no faster than streaming twice on
+        // 98-125 KB rows (bf16 0.70-0.83 against 0.78-0.89).
         int lists = 0;
         r.cluster = 1;
-        for (int nt : {128, 256, 512, 0}) {
-            r.resident = nt != 0;
-            r.ring_threads = nt ? nt : 512;
-            lists = list_warps(r.ring_threads) * list_bytes(words, r.table_bits);
-            const int room = (kSmemPerSm * r.ring_threads / 512 - kSmemReserve - lists) /
-                             chunk_bytes(r.ring_threads, r.resident);
+        for (int nt : {128, 256, 512}) {
+            r.ring_threads = nt;
+            lists = list_warps(nt) * list_bytes(words, r.table_bits);
+            const int room = (kSmemPerSm * nt / 512 - kSmemReserve - lists) / chunk_bytes(nt);
             r.slots = room < kMaxSlots ? room : kMaxSlots;
-            const long long held = (long long)r.slots * chunk_bytes(r.ring_threads, true);
-            if (!r.resident || row * (nt == 512 ? 17 : 10) <= held * 10) break;
+            if (row <= (long long)r.slots * chunk_bytes(nt)) break;
         }
-        r.smem = r.slots * chunk_bytes(r.ring_threads, r.resident) + lists;
+        r.smem = r.slots * chunk_bytes(r.ring_threads) + lists;
     }
     const int groups = r.group == 32 ? 8 : 1;
     if (!r.ring_threads)

@@ -22,10 +22,11 @@ struct DistillParams : ParamsEx {
 // How a row is spread: `group` threads (32: a warp per row, eight rows per
 // CTA; else one CTA per row) of `vecs` 16-byte vectors each; `cluster` CTAs
 // per row; `loop`: rows longer than the registers hold, read twice.
-// `ring_threads` (else 0): rows go through a ring of `slots` chunks instead.
+// `ring_threads` (else 0): rows go through a ring of `slots` chunks instead (of
+// 512 threads: streamed twice).
 struct DistillPlan {
     int group, vecs, cluster;
-    bool loop, resident;
+    bool loop;
     int ring_threads, slots, table_bits;
     int ctas;
     int smem;
