@@ -238,15 +238,28 @@ __device__ __forceinline__ void epi_tile_max(const HeadGemm &p, const HeadWork &
     }
 }
 
-// Few rows: this lane's class against 32 rows of the batch.  A row's maximum
+// Few rows: stages k, k + 4, .. of a contraction add to an accumulator of their
+// own (64 columns each; tensor memory has the room), and the four sums are
+// added in fp32.  The tensor core's additions cut off low bits: on 64 rows x
+// 128256 classes x 4096 the loss was off by 2.8e-6 with one accumulator.
+constexpr int kScoreChains = 4;
+
+// This lane's class against 32 rows of the batch.  A row's maximum
 // and sum over the warp's classes: one reduction instruction per row for the
 // maximum, a transposing tree of shuffles (lane i ends with row i) for the sum.
 __device__ __forceinline__ void epi_score(const HeadGemm &p, const Unit &u, uint32_t acc,
-                                          int class0, int classes, int stat, int row0) {
+                                          int class0, int classes, int stat, int row0,
+                                          int chains) {
     const int lane = threadIdx.x & 31;
     float v[32], e[32];
     tmem_ld32(acc + row0, v);
     tmem_wait_ld(v);
+    for (int i = 1; i < chains; ++i) {
+        tmem_ld32(acc + i * kScoreRows + row0, e);
+        tmem_wait_ld(e);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += e[j];
+    }
     const int row = row0 + lane;
     int target = -1;
     if (p.targets != nullptr && row < p.rows) target = __ldg(p.targets + p.first + row);
@@ -544,8 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int ab = it & 1;
             if (!(ok = wait_or_fail(p, &bar.acc_empty[ab], ((it >> 1) & 1) ^ 1))) break;
             tc_fence_after();
-            const uint32_t d = tmem + ab * kTileN;
+            constexpr int kChains = PROD == kProdScore ? kScoreChains : 1;
             for (int k = u.k0; k < u.k1; ++k) {
+                const uint32_t d = tmem + ab * kTileN +
+                                   (kChains > 1 ? (k % kChains) * kScoreRows : 0);
                 if (!(ok = wait_or_fail(p, &bar.full[s], ph))) break;
                 tc_fence_after();
                 const uint32_t a = smem_addr(smem + s * kStageBytes);
@@ -556,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                              : smem_desc(a + kk * 32, 16, 1024);
                     const uint64_t bd = kBMn ? smem_desc(b + kk * 2048, kOperandBytes / 2, 1024)
                                              : smem_desc(b + kk * 32, 16, 1024);
-                    mma_pair(d, ad, bd, idesc, k > u.k0 || kk > 0);
+                    mma_pair(d, ad, bd, idesc, k >= u.k0 + kChains || kk > 0);
                 }
                 commit_pair(&bar.empty[s]);
                 if (++s == kStages) {
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int classes = min(half_m - quad * 32, p.C - class0);
                 for (int r0 = half * 32; r0 < work.rows; r0 += 64)
                     epi_score(p, u, tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN, class0,
-                              classes, rank * 4 + quad, r0);
+                              classes, rank * 4 + quad, r0, min(kScoreChains, work.k_blocks));
             } else if (m0 < rows) {
                 if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, half, st);
