@@ -45,6 +45,23 @@ int ce_fwd_bwd_test(const void *logits, const int32_t *targets, int64_t B, int64
                     float *loss_out, void *grad_out, void *stream, int path, int split,
                     const ce_test_hooks *hooks);
 
+/*
+ * ce_heads_test -- from now on, in calls of ce_linear_fwd_bwd,
+ * ce_linear_distill_fwd_bwd and ce_distill_fwd_bwd of this process:
+ *   skip_copy          >= 0: a copy is never issued, so the waits for it must
+ *                      give up (the call counts timeouts and its loss, or every
+ *                      row's, is NaN): the first stage of the logits' product
+ *                      of the rows from this one on in steps of 256; or, of a
+ *                      batch that ce_distill_fwd_bwd streams through shared
+ *                      memory, the first chunk of this row.  -1: none.
+ *   wait_limit_cycles  0: the library's limit (about a second); otherwise the
+ *                      number of SM clock cycles after which a wait gives up
+ *                      (waits for copies in flight after that keep the
+ *                      library's).
+ * (-1, 0) restores the ordinary state.  Not for concurrent use.
+ */
+int ce_heads_test(int64_t skip_copy, int64_t wait_limit_cycles);
+
 #ifdef __cplusplus
 }
 #endif

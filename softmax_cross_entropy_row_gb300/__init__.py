@@ -56,7 +56,7 @@ EXPORTS = ("ce_fwd_bwd", "ce_fwd_bwd_path", "ce_query_plan", "ce_get_device_erro
            "ce_fwd_bwd_host_grad", "ce_linear_fwd_bwd", "ce_distill_fwd_bwd",
            "ce_linear_distill_fwd_bwd")
 # Symbols declared in include/ce_testing.h (test hooks).
-TEST_EXPORTS = ("ce_fwd_bwd_test",)
+TEST_EXPORTS = ("ce_fwd_bwd_test", "ce_heads_test")
 
 
 class TestHooks(ctypes.Structure):
@@ -133,6 +133,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.ce_fwd_bwd_test.argtypes = [vp, vp, i64, i64, ci, vp, vp, vp, ci, ci,
                                     ctypes.POINTER(TestHooks)]
     lib.ce_fwd_bwd_test.restype = ci
+    lib.ce_heads_test.argtypes = [i64, i64]
+    lib.ce_heads_test.restype = ci
     if path is None:
         _lib = lib
     return lib
@@ -368,6 +370,12 @@ def ce_fwd_bwd_test(logits, targets, loss_out, grad_out, stream=None, path=CE_PA
     _check(lib.ce_fwd_bwd_test(_ptr(logits), _ptr(targets), B, C, _dtype_code(logits),
                                _ptr(loss_out), _ptr(grad_out), _stream_handle(stream), int(path),
                                int(split), ctypes.byref(hooks)))
+
+
+def ce_heads_test(skip_copy=-1, wait_limit_cycles=0) -> None:
+    """The test hooks of the projection's and the teacher's calls (see
+    include/ce_testing.h); without arguments: none.  Tests only."""
+    _check(load_library().ce_heads_test(int(skip_copy), int(wait_limit_cycles)))
 
 
 def _check_heads(rows, reduction, loss_out, grad_scale, **others) -> None:

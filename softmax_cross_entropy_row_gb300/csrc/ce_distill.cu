@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
         atomicAdd(&p.err[kErrTimeout], 1);
     };
     auto is_dead = [&] { return *reinterpret_cast<volatile int *>(&dead) != 0; };
+    const long long limit = p.copy_wait_limit;
     const float scale = p.exp_scale;
     const bool grads = writes_grad(p);
     const int passes = grads && !RESIDENT ? 2 : 1;
@@ -662,13 +663,16 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                 for (int pass = 0; pass < passes; ++pass) {
                     const uint64_t policy = pass + 1 < passes ? keep : drop;
                     for (long long v = 0; v < sp.v1; v += VC) {
-                        if (!mbar_wait(&empty[s], ph ^ 1u)) {
+                        if (!mbar_wait(&empty[s], ph ^ 1u, limit)) {
                             fail();
                             goto copied;
                         }
                         const uint32_t bytes = (uint32_t)min((long long)VC, sp.v1 - v) * 16u;
-                        mbar_arrive_expect_tx(&full[s], bytes);
-                        bulk_g2s_hint(ring + (size_t)s * CH, v0 + v * 16, bytes, &full[s], policy);
+                        if (!(skips_copy(p, b, b + 1) && v == 0 && pass == 0)) {
+                            mbar_arrive_expect_tx(&full[s], bytes);
+                            bulk_g2s_hint(ring + (size_t)s * CH, v0 + v * 16, bytes, &full[s],
+                                          policy);
+                        }
                         ++issued;
                         if (++s == S) {
                             s = 0;
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             if (merge_list(l, words, rs.table_bits))
                 for (int k = lane; k < words; k += 32)
                     l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
-            if (!__all_sync(0xffffffffu, mbar_wait(&row_done[j], ph))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&row_done[j], ph, limit))) {
                 if (lane == 0) fail();
                 break;
             }
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
         // at its next barrier, where all warps see the same flags.
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
             return ok;
         };
         for (long long b = blockIdx.x; b < p.B; b += gridDim.x) {

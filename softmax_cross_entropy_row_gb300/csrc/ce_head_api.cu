@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/ce.h"
+#include "../../include/ce_testing.h"
 #include "ce_distill.h"
 #include "ce_head_gemm.h"
 #include "ce_head_rows.h"
@@ -35,6 +36,7 @@ struct Buffer {
     size_t bytes = 0;
 };
 std::mutex g_mu;  // held over a whole call: its launches use the workspace
+long long g_skip_copy = -1, g_wait_limit = 0;  // ce_heads_test, under g_mu
 std::map<std::tuple<int, uintptr_t, unsigned long long>, Buffer> g_buffers;
 std::vector<std::pair<int, unsigned char *>> g_outgrown;  // of captures
 
@@ -443,6 +445,8 @@ int run(const Call &c) {
         g.err = err;
         g.parts = ws.parts;
         g.dhidden = static_cast<unsigned char *>(c.dhidden);
+        g.skip_row = (int)std::max(-1LL, g_skip_copy >= 0 ? g_skip_copy - b0 : -1LL);
+        g.wait_limit = g_wait_limit > 0 ? g_wait_limit : ce::kWaitLimitCycles;
         g.clear_failed = i == 0;
         g.clear_rescue = z.per_row;
         if (z.score) {
@@ -515,6 +519,7 @@ int run(const Call &c) {
         if (teacher) CE_CUDA(ce::launch_head_listed(r, bf16, s));
 
         g.clear_failed = g.clear_rescue = 0;
+        g.skip_row = -1;
         if (c.dhidden) {
             CE_TRY(tensor_map(&g.a, c.dtype, ws.exps, padded, z.ld, z.ld, ce::kTileM / 2));
             CE_TRY(tensor_map(&g.b, c.dtype, c.weight, c.C, c.D, c.D, ce::kTileK));
@@ -648,6 +653,8 @@ int run(const DistillCall &c) {
     p.list_words = (int)round_up(c.K, 4);
     p.temperature = c.temperature;
     p.exp_scale = ce::kLog2e / c.temperature;
+    p.skip_copy_row = g_skip_copy;
+    if (g_wait_limit > 0) p.copy_wait_limit = g_wait_limit;
     CE_CUDA(ce::launch_distill(p, c.dtype, plan, s));
     return CE_OK;
 }
@@ -724,6 +731,13 @@ int ce_distill_fwd_bwd(const void *logits, const int32_t *teacher_idx, const voi
     c.grad = grad_out;
     c.stream = stream;
     return run(c);
+}
+
+int ce_heads_test(int64_t skip_copy, int64_t wait_limit_cycles) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_skip_copy = skip_copy >= 0 ? skip_copy : -1;
+    g_wait_limit = wait_limit_cycles > 0 ? wait_limit_cycles : 0;
+    return CE_OK;
 }
 
 int ce_linear_distill_fwd_bwd(const void *hidden, const void *weight, const int32_t *teacher_idx,

@@ -435,8 +435,8 @@ __device__ __forceinline__ void epi_f32(const HeadGemm &p, const Unit &u, uint32
 // Waits that give up end the role's loop; every other role then gives up at
 // its own next wait, so all threads reach the end of the kernel.
 __device__ __forceinline__ bool wait_or_fail(const HeadGemm &p, uint64_t *bar, uint32_t parity,
-                                             long long limit = kWaitLimitCycles) {
-    if (mbar_wait_limit(bar, parity, limit)) return true;
+                                             long long more = 0) {
+    if (mbar_wait_limit(bar, parity, p.wait_limit + more)) return true;
     *reinterpret_cast<volatile int *>(p.failed) = 1;
     atomicAdd(&p.err[kErrTimeout], 1);
     return false;
@@ -511,22 +511,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const int n0 = u.nt * p.tile_n + rank * half_n;
             for (int k = u.k0; k < u.k1; ++k) {
                 if (!(ok = wait_or_fail(p, &bar.empty[s], ph ^ 1u))) break;
-                if (rank == 0)
+                // test hook: this stage's copies are left out
+                const bool skip_copy = p.skip_row >= 0 && k == u.k0 &&
+                                       u.mt * p.tile_m == p.skip_row / kTileM * kTileM;
+                if (rank == 0 && !skip_copy)
                     mbar_arrive_expect_tx(&bar.full[s], 2 * (half_m + half_n) * kTileK * 2);
                 const uint32_t fb = mapa(&bar.full[s], 0);
-                unsigned char *da = smem + s * kStageBytes;
-                unsigned char *db = da + kOperandBytes;
-                if constexpr (kAMn) {
-                    tma_load_pair(da, map_a, m0, k * kTileK, fb);
-                    tma_load_pair(da + kOperandBytes / 2, map_a, m0 + 64, k * kTileK, fb);
-                } else {
-                    tma_load_pair(da, map_a, k * kTileK, m0, fb);
-                }
-                if constexpr (kBMn) {
-                    tma_load_pair(db, map_b, n0, k * kTileK, fb);
-                    tma_load_pair(db + kOperandBytes / 2, map_b, n0 + 64, k * kTileK, fb);
-                } else {
-                    tma_load_pair(db, map_b, k * kTileK, n0, fb);
+                if (!skip_copy) {
+                    unsigned char *da = smem + s * kStageBytes;
+                    unsigned char *db = da + kOperandBytes;
+                    if constexpr (kAMn) {
+                        tma_load_pair(da, map_a, m0, k * kTileK, fb);
+                        tma_load_pair(da + kOperandBytes / 2, map_a, m0 + 64, k * kTileK, fb);
+                    } else {
+                        tma_load_pair(da, map_a, k * kTileK, m0, fb);
+                    }
+                    if constexpr (kBMn) {
+                        tma_load_pair(db, map_b, n0, k * kTileK, fb);
+                        tma_load_pair(db + kOperandBytes / 2, map_b, n0 + 64, k * kTileK, fb);
+                    } else {
+                        tma_load_pair(db, map_b, k * kTileK, n0, fb);
+                    }
                 }
                 ++issued;
                 if (++s == kStages) {
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         float f = 1.f;
         if constexpr (EPI == kEpiOut) f = p.alpha * p.info->out;
         // a whole contraction may lie between two finished accumulators
-        const long long acc_limit = kWaitLimitCycles + 4096LL * work.k_blocks;
+        const long long acc_more = 4096LL * work.k_blocks;
         // rows of the product; of the logits also those up to the next 64,
         // whose kept exponentials are zeros (the last stage of E^T H reads them)
         const int rows = PROD == kProdWeight ? p.C
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int w = pair; w < units; w += pairs, ++it) {
             const Unit u = unit_of(p, work, w);
             const int ab = it & 1;
-            if (!wait_or_fail(p, &bar.acc_full[ab], (it >> 1) & 1, acc_limit)) break;
+            if (!wait_or_fail(p, &bar.acc_full[ab], (it >> 1) & 1, acc_more)) break;
             tc_fence_after();
             const uint32_t acc =
                 tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN + half * (p.tile_n / 2);

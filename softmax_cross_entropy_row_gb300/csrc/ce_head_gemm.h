@@ -77,6 +77,8 @@ struct HeadGemm {
     int row_mul_stride;
     unsigned char *dhidden;        // [B][D]
     int *failed, *rescue;
+    long long wait_limit;          // cycles after which a wait gives up
+    int skip_row;                  // test hook: the tile row from this row on lacks a copy; -1
     int *err;                      // error counters
 };
 
