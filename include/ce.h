@@ -333,10 +333,11 @@ int ce_fwd_bwd_noalloc(const void *logits, const int32_t *targets, int64_t B, in
  *
  * Workspace: the library keeps one per stream, allocated by the first call
  * that needs it and replaced by a larger one when a call needs more (both may
- * synchronise): with gradients 2 C bytes for each row of a piece, where a
- * piece has at most 1 GiB or, with dweight, 4 C D bytes (or 256 rows), and 4 C
- * D bytes more when dweight is formed from several pieces.  A call captured
- * into a graph allocates a workspace of its own, which lives until
+ * synchronise).  With gradients it holds 80 MB, 2 D bytes for each row, 2 D
+ * and 2 C bytes for each row of a piece, where a piece's 2 C bytes are at most
+ * 1 GiB or, with dweight, 4 C D bytes (or 256 rows), and 4 C D bytes when
+ * dweight is formed from several pieces.  A call captured into a graph
+ * allocates a workspace of its own, which lives until
  * ce_release_workspaces: such graphs may be replayed on any stream, at the
  * same time as other calls.  The device error counters are the stream's.
  */

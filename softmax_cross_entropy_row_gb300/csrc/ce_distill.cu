@@ -227,7 +227,7 @@ __device__ __forceinline__ ListSums take_list(const DistillParams &p, long long 
     return r;
 }
 
-// The row of this warp after next on its way to L2: its list.
+// The list of a later row on its way to L2.
 __device__ __forceinline__ void prefetch_list(const DistillParams &p, long long b) {
     const int vs = p.val_dtype == 0 ? 4 : 2;
     prefetch_l2(p.idx + b * p.K, 4LL * p.K);
@@ -362,7 +362,8 @@ constexpr int min_ctas(int g, int v, bool loop) {
 }
 
 template <typename T, int G, int V, bool LOOP>
-__global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP)) distill_kernel(DistillParams p, int cluster, int bits) {
+__global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP))
+    distill_kernel(DistillParams p, int cluster, int bits) {
     using E = Elem<T>;
     constexpr int ES = E::kBytes;
     constexpr int NT = G == 32 ? 256 : G;

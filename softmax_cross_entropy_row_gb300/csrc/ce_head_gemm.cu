@@ -25,7 +25,7 @@
 namespace ce {
 namespace {
 
-constexpr int kCtaRows = kTileM / 2;               // rows of A and of B per CTA
+constexpr int kCtaRows = kTileM / 2;                  // rows of A and of B per CTA
 constexpr int kOperandBytes = kCtaRows * kTileK * 2;  // 16 KB
 // The ring: six stages of 16 + 16 KB; with few rows as B eleven of 16 + 4 KB.
 constexpr int kMaxStages = 11;
@@ -47,7 +47,9 @@ struct Barriers {
     uint32_t tmem;
 };
 
-__host__ __device__ constexpr int box_bytes(int prod) { return prod == kProdScore ? 0 : kEpiWarps * kEpiBufBytes; }
+__host__ __device__ constexpr int box_bytes(int prod) {
+    return prod == kProdScore ? 0 : kEpiWarps * kEpiBufBytes;
+}
 constexpr int smem_bytes(int prod) {
     return stages_of(prod) * stage_bytes(prod) + box_bytes(prod) + 1024 /* alignment */ +
            (int)sizeof(Barriers);
@@ -489,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (p.clear_failed) *reinterpret_cast<volatile int *>(p.failed) = 0;
         if (p.clear_rescue) *reinterpret_cast<volatile int *>(p.rescue) = 0;
     }
-    const bool skip = p.only_if != nullptr && *reinterpret_cast<const volatile int *>(p.only_if) == 0;
+    const bool skip =
+        p.only_if != nullptr && *reinterpret_cast<const volatile int *>(p.only_if) == 0;
     const int count = p.dynamic ? p.info->count : p.B;
     const bool packed = count < p.B;
     const HeadWork work = head_work(p, (HeadProduct)PROD, count, pairs);
@@ -620,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     epi_score(p, u, tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN, class0,
                               classes, rank * 4 + quad, r0, min(kScoreChains, work.k_blocks));
             } else if (m0 < rows) {
-                if constexpr (EPI == kEpiStats) epi_tile_max<E, false>(p, work, u, acc, m0, half, st);
-                if constexpr (EPI == kEpiKeep) epi_tile_max<E, true>(p, work, u, acc, m0, half, st);
+                if constexpr (EPI == kEpiStats || EPI == kEpiKeep)
+                    epi_tile_max<E, EPI == kEpiKeep>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiRef) epi_ref<E>(p, work, u, acc, m0, half, st);
                 if constexpr (EPI == kEpiOut) {
                     if (u.part >= 0)

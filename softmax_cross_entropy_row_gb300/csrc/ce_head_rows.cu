@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(256) head_rows_kernel(HeadRows p) {
         const float mass = fabsf(p.mass[b]);
         out.M = a.M;
         out.mul = mass * w / a.S * (per_row ? 1.f : p.shift_mul);
-        // what a listed class's (mass p - q) is multiplied by to be kept
-        out.target = per_row ? a.S / mass : w * p.shift_mul;
+        // what a listed class's p - q / mass (mass p - q) is multiplied by to be kept
+        out.target = per_row ? a.S : w * p.shift_mul;
         out.log2S = log2f(a.S);
     }
     p.row[row] = out;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(256) head_listed_kernel(HeadRows p) {
         }
         if (first)
             E::store(p.exps + ((size_t)row * p.ld + c) * 2,
-                     (mass * ex2(lp2) - all) * h.target);
+                     (p.ref ? ex2(lp2) - all / mass : mass * ex2(lp2) - all) * h.target);
     }
     l = warp_sum(l);
     if (lane == 0) {

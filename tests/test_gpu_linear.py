@@ -265,6 +265,39 @@ def test_same_bits_each_time_and_on_another_stream():
             assert all(torch.equal(a, b) for a, b in zip(out, first))
 
 
+def test_calls_from_two_threads():
+    """Two host threads with a stream each, and two on one stream."""
+    import threading
+
+    cases = []
+    for seed in (1, 2):
+        t = some_targets(400 * seed, 1500, seed, ignored=0.2)
+        h, w = heads.projection(400 * seed, 128, 1500, "bf16", seed, raised=t)
+        cases.append((h, w, t, check_linear(h, w, t, "bf16")))
+    own = [torch.cuda.Stream() for _ in cases]
+    shared = torch.cuda.Stream()
+    for streams in (own, [shared, shared]):
+        wrong = []
+
+        def work(i):
+            h, w, t, want = cases[i]
+            for _ in range(20):
+                with torch.cuda.stream(streams[i]):
+                    out = [torch.empty_like(x) for x in want]
+                    ce.ce_linear_fwd_bwd(h, w, t, *out, stream=streams[i])
+                    if not all(torch.equal(a, b) for a, b in zip(out, want)):
+                        wrong.append(i)
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        torch.cuda.synchronize()
+        for th in threads:
+            th.start()
+        for th in threads:
+            th.join()
+        torch.cuda.synchronize()
+        assert not wrong
+
+
 def test_graphs_replayed_at_the_same_time():
     """Two captured calls (the stream's first) replayed on two streams while an
     eager call runs: each has a workspace of its own.  A replay sees changed
@@ -454,6 +487,24 @@ def test_linear_distill_repeated_and_bad_classes(dtype):
     ce.ce_get_device_errors()
     check_linear_distill(h, w, idx, val, dtype, reduction=NONE)
     assert ce.ce_get_device_errors() == (3, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("away", [-2.0, 60.0, 95.0])
+def test_lists_of_another_mass(dtype, away):
+    """A normaliser that is not the list's: masses of e^2, e^-60 and e^-95 (a
+    number without all its bits)."""
+    B, D, C, K = 60, 64, 300, 5
+    idx, val = heads.teacher_lists(B, C, K, 4)
+    h, w = heads.projection(B, D, C, dtype, 4)
+    lse = torch.logsumexp(val, 1) + away
+    if away < 90:
+        check_linear_distill(h, w, idx, val, dtype, lse, reduction=SUM)
+        return
+    loss, dh, dw = outputs(h, w, NONE)
+    ce.ce_linear_distill_fwd_bwd(h, w, idx, val, loss, dh, dw, teacher_lse=lse, reduction=NONE)
+    for x in (loss, dh, dw):
+        assert x.float().abs().max() < 1e-36
 
 
 def test_linear_distill_far_from_its_teacher():
