@@ -380,30 +380,37 @@ __device__ __forceinline__ void epi_hidden(const HeadGemm &p, const HeadWork &w,
     }
 }
 
-// The weights' gradient in 16 bits (`zero`: no row counts).
-template <typename E>
+// The weights' gradient in 16 bits (`zero`: no row counts).  All 128 columns are
+// read first and the accumulator is handed back (`release`) before they are
+// stored.
+template <typename E, typename R>
 __device__ __forceinline__ void epi_weight(const HeadGemm &p, const Unit &u, uint32_t acc, int m0,
-                                           int half, float f, bool zero, Stager &st) {
+                                           int half, float f, bool zero, Stager &st, R release) {
     const int lane = threadIdx.x & 31;
-    float v[32];
+    float v[4][32];
     const int n0 = u.nt * kTileN + half * kStatN;
     const int cols = min(kStatN, p.D - n0);
-#pragma unroll 1
-    for (int c0 = 0; c0 < cols; c0 += 64) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            tmem_ld32(acc + c0 + 32 * h, v);
-            tmem_wait_ld(v);
-            if (h == 0) st.open();
+    for (int i = 0; i < 4; ++i) tmem_ld32(acc + 32 * i, v[i]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[8];
+    for (int i = 0; i < 4; ++i) tmem_wait_ld(v[i]);
+    release();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = zero ? 0.f : f * v[8 * q + i];
-                stage16(st.box, lane, 4 * h + q, E::pack(x));
-            }
+    for (int c = 0; c < 2; ++c) {
+        if (c * 64 >= cols) break;
+        uint4 w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = zero ? 0.f : f * v[2 * c + q / 4][q % 4 * 8 + i];
+            w[q] = E::pack(x);
         }
-        st.close([&](const void *src) { tma_store(&p.out, src, n0 + c0, m0); });
+        st.open();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) stage16(st.box, lane, q, w[q]);
+        st.close([&](const void *src) { tma_store(&p.out, src, n0 + 64 * c, m0); });
     }
 }
 
@@ -615,6 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tmem + ((uint32_t)(quad * 32) << 16) + ab * kTileN + half * (p.tile_n / 2);
             const int row0 = rank * kCtaRows + quad * 32;
             const int m0 = u.mt * kTileM + row0;
+            bool released = false;
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa(&bar.acc_empty[ab], 0));
+                released = true;
+            };
             if constexpr (PROD == kProdScore) {
                 // this warp's classes, and every second 32 rows of the batch
                 const int class0 = u.mt * p.tile_m + rank * half_m + quad * 32;
@@ -632,14 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     else if constexpr (PROD == kProdHidden)
                         epi_hidden<E>(p, work, u, acc, m0, half, f, st);
                     else
-                        epi_weight<E>(p, u, acc, m0, half, f, zero, st);
+                        epi_weight<E>(p, u, acc, m0, half, f, zero, st, release);
                 }
                 if constexpr (EPI == kEpiF32) epi_f32<false>(p, u, acc, m0, half, zero, st);
                 if constexpr (EPI == kEpiAdd) epi_f32<true>(p, u, acc, m0, half, zero, st);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa(&bar.acc_empty[ab], 0));
+            if (!released) release();
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
