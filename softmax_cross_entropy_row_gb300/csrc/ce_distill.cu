@@ -234,6 +234,17 @@ __device__ __forceinline__ void prefetch_list(const DistillParams &p, long long 
     prefetch_l2(static_cast<const unsigned char *>(p.val) + b * p.K * vs, (long long)vs * p.K);
 }
 
+// The reducing warps' shares of a row, joined by every lane of a warp.
+template <int NW>
+__device__ __forceinline__ MS join_parts(const MS *part, float scale) {
+    const int lane = threadIdx.x & 31;
+    const MS w = lane < NW ? part[lane] : MS{-INFINITY, 0.f};
+    MS a;
+    a.m = warp_max(w.m);
+    a.s = warp_sum(w.m == -INFINITY ? w.s : w.s * ex2((w.m - a.m) * scale));
+    return a;
+}
+
 // A row's place in memory: nh elements up to a 16-byte boundary, nvec whole
 // vectors, the rest; this CTA's share is vectors [v0, v1) and, at the ends,
 // the loose elements: elements [e0, e1).
@@ -449,9 +460,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G, min_ctas(G, V, LOOP))
         if constexpr (G > 32) {
             if (lane == 0) part[buf][warp] = a;
             __syncthreads();
-            const MS w = lane < WARPS ? part[buf][lane] : MS{-INFINITY, 0.f};
-            a.m = warp_max(w.m);
-            a.s = warp_sum(w.m == -INFINITY ? w.s : w.s * ex2((w.m - a.m) * scale));
+            a = join_parts<WARPS>(part[buf], scale);
             if (cluster > 1) {
                 if (threadIdx.x == 0) mine[buf] = make_float4(a.m, a.s, 0.f, 0.f);
                 cluster_sync();
@@ -615,8 +624,8 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
     __shared__ uint64_t list_full[LW], row_done[LW];
     __shared__ MS joined[LW];
     __shared__ float masses[LW];
-    __shared__ MS part[2][NW];
-    __shared__ int fine[2][NW];  // the warp's waits have all been met
+    __shared__ MS part[LW][NW];
+    __shared__ int fine[LW][NW];  // the warp's waits have all been met
     __shared__ int dead;  // a wait gave up
     __shared__ int tail_flag;
     __shared__ float2 tail_scratch[kTailWarps];
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                 if (lane == 0) fail();
                 break;
             }
-            const MS a = joined[j];
+            const MS a = grads ? joined[j] : join_parts<NW>(part[j], scale);
             const float f = row_grad_factor(p, scalar, b) * p.temperature;
             const float log2S = log2f(a.s);
             float cross = 0.f;
@@ -750,7 +759,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
         // ---- the rows
         const int t = threadIdx.x;
         const float scalar = scalar_grad_scale(p);
-        int s = 0, buf = 0, lb = 0;
+        int s = 0, lb = 0;
         uint32_t ph = 0, lph = 0;
         // A wait that gave up ends the warp's part in this row; the CTA stops
         // at its next barrier, where all warps see the same flags.
@@ -825,14 +834,24 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             const float wm = warp_max(a.m);
             a.s = warp_sum(wm == -INFINITY ? a.s : a.s * ex2((a.m - wm) * scale));
             if (lane == 0) {
-                part[buf][warp] = {wm, a.s};
-                fine[buf][warp] = ok;
+                part[lb][warp] = {wm, a.s};
+                fine[lb][warp] = ok;
+            }
+            auto next_list = [&] {
+                if (++lb == LW) {
+                    lb = 0;
+                    lph ^= 1u;
+                }
+            };
+            if (!grads) {  // the list's warp joins the parts: no barrier
+                if (!ok) break;
+                release_row(lb);
+                next_list();
+                continue;
             }
             named_sync(1, NT);
-            const MS w = lane < NW ? part[buf][lane] : MS{-INFINITY, 0.f};
-            if (!__all_sync(0xffffffffu, lane >= NW || fine[buf][lane])) break;
-            a.m = warp_max(w.m);
-            a.s = warp_sum(w.m == -INFINITY ? w.s : w.s * ex2((w.m - a.m) * scale));
+            if (!__all_sync(0xffffffffu, lane >= NW || fine[lb][lane])) break;
+            a = join_parts<NW>(part[lb], scale);
             const float m = a.m;
             const float inv = 1.f / a.s;
             const float mass = masses[lb];
@@ -891,11 +910,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
             }
             if (threadIdx.x == 0) joined[lb] = a;
             release_row(lb);
-            buf ^= 1;
-            if (++lb == LW) {
-                lb = 0;
-                lph ^= 1u;
-            }
+            next_list();
         }
     }
     __syncthreads();
