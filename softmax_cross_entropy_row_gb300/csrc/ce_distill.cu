@@ -171,9 +171,10 @@ __device__ __forceinline__ void clear_table(const List &l, int bits) {
 // cls and prob with the places of a class added up, by one warp (the table has
 // been cleared).  A hash table finds out whether any class is listed twice.
 // Only then the later places' probabilities are added to the first's, as
-// multiples of 2^-40, whose sums do not depend on the order of the additions
-// (z is formed anew then).  Returns whether that was so.
-__device__ __forceinline__ bool merge_list(const List &l, int words, int bits) {
+// multiples of 2^-61 of the list's mass (a power of two above it), whose sums do
+// not depend on the order of the additions (z is formed anew then).  Returns
+// whether that was so.
+__device__ __forceinline__ bool merge_list(const List &l, int words, int bits, float mass) {
     const int lane = threadIdx.x & 31;
     const int size = 1 << bits;
     bool twice = false;
@@ -190,7 +191,9 @@ __device__ __forceinline__ bool merge_list(const List &l, int words, int bits) {
     }
     twice = __any_sync(0xffffffffu, twice);
     if (twice) {
-        constexpr float kUnit = 1099511627776.f;  // 2^40
+        // 2^(61 - e), mass < 2^e (any scale will do for a mass that is none)
+        const int e = (int)(__float_as_uint(mass) >> 23 & 255u) - 126;
+        const float unit = e > -60 && e < 120 ? exp2f((float)(61 - e)) : 1.f;
         for (int i = lane; i < size; i += 32) l.first[i] = words;
         for (int k = lane; k < words; k += 32) l.acc[k] = 0ull;
         __syncwarp();
@@ -202,12 +205,12 @@ __device__ __forceinline__ bool merge_list(const List &l, int words, int bits) {
             const int f = l.first[find(l.key, bits, l.cls[k])];
             if (f == k) continue;
             const float q = l.prob[k];
-            atomicAdd(&l.acc[f], (unsigned long long)(fminf(q, 1048576.f) * kUnit));
+            atomicAdd(&l.acc[f], (unsigned long long)fminf(q * unit, 4.611686e18f));  // 2^62
             l.cls[k] = -1;
         }
         __syncwarp();
         for (int k = lane; k < words; k += 32)
-            l.prob[k] += (float)((double)l.acc[k] * (1.0 / (double)kUnit));
+            l.prob[k] += (float)((double)l.acc[k] / (double)unit);
         __syncwarp();
     }
     return twice;
@@ -220,7 +223,7 @@ __device__ __forceinline__ ListSums take_list(const DistillParams &p, long long 
     const int words = p.list_words;
     clear_table(l, bits);
     const ListSums r = read_list<E>(p, b, l.cls, l.prob, l.z, row);
-    if (merge_list(l, words, bits))  // z lies in the sums' place
+    if (merge_list(l, words, bits, r.mass))  // z lies in the sums' place
         for (int k = threadIdx.x & 31; k < words; k += 32)
             l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * E::kBytes) : 0.f;
     __syncwarp();
@@ -677,6 +680,12 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                             fail();
                             goto copied;
                         }
+                        // The slot was read through the generic proxy and is
+                        // written through the async one: without this fence the
+                        // next row's bytes could arrive before the last reads of
+                        // this row's (seen with gradients stored element by
+                        // element, whose stores hold the reads up).
+                        fence_proxy_async();
                         const uint32_t bytes = (uint32_t)min((long long)VC, sp.v1 - v) * 16u;
                         if (!(skips_copy(p, b, b + 1) && v == 0 && pass == 0)) {
                             mbar_arrive_expect_tx(&full[s], bytes);
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(NT + 32 + 32 * list_warps(NT), 512 / NT)
                 masses[j] = mass;
                 mbar_arrive(&list_full[j]);  // the reducing warps need the mass alone
             }
-            if (merge_list(l, words, rs.table_bits))
+            if (merge_list(l, words, rs.table_bits, mass))
                 for (int k = lane; k < words; k += 32)
                     l.z[k] = l.cls[k] >= 0 ? E::load_global(row + (size_t)l.cls[k] * ES) : 0.f;
             if (!__all_sync(0xffffffffu, mbar_wait(&row_done[j], ph, limit))) {
@@ -973,9 +982,9 @@ cudaError_t resident(const void *f, int threads, int smem, int *n) {
 }  // namespace
 
 // Shared memory of an SM, and what a CTA of the ring needs beside the ring
-// and its lists (the system's 1 KB and the kernel's static part).
+// and its lists (the system's 1 KB and the kernel's static part, under 2 KB).
 constexpr int kSmemPerSm = 228 * 1024;
-constexpr int kSmemReserve = 2048;
+constexpr int kSmemReserve = 3072;
 
 cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
                          DistillPlan *pl) {

@@ -135,6 +135,49 @@ def test_lists_longer_than_the_row(B, C, K):
         check_distill(student(B, C, dtype, 6), idx, val, dtype, reduction=NONE)
 
 
+@pytest.mark.parametrize("B,C,dtype", [(460, 45362, "f16"), (741, 41035, "f16"),
+                                       (620, 24577, "f32"), (500, 60001, "bf16")])
+def test_slots_are_not_refilled_while_they_are_read(B, C, dtype):
+    """Rows that fill the ring, a gradient aligned unlike the logits (stored
+    element by element, slowly): every run has the first one's bits."""
+    idx, val = heads.teacher_lists(B, C, 2, 1)
+    buf = torch.randn(B * C + 8, device="cuda").mul_(3).to(heads.TORCH_DT[dtype])
+    z = buf[1:1 + B * C].view(B, C)
+    loss, grad = check_distill(z, idx, val, dtype, reduction=NONE)
+    again = torch.empty_like(grad)
+    for _ in range(150):
+        again.fill_(7)
+        ce.ce_distill_fwd_bwd(z, idx, val, loss, again, reduction=NONE)
+        assert torch.equal(again, grad)
+
+
+def test_every_list_length_fits():
+    """The ring's shared memory for any K (its lists take what the row's chunks
+    leave), on rows of each of its kernels."""
+    for C in (9000, 20000, 110001):
+        z = student(160, C, "bf16", C)
+        loss = torch.empty(160, device="cuda")
+        for K in range(1, 1025, 7):
+            idx, val = heads.teacher_lists(160, C, K, K)
+            loss.fill_(math.nan)
+            ce.ce_distill_fwd_bwd(z, idx, val, loss, reduction=NONE)
+            assert torch.isfinite(loss).all(), (C, K)
+
+
+@pytest.mark.parametrize("B,C", KERNELS)
+def test_small_probabilities_of_repeated_classes(B, C):
+    """Sums of places of one class keep their bits however small they are."""
+    g = torch.Generator("cuda").manual_seed(7)
+    K = 120
+    idx = torch.randint(0, 60, (B, K), generator=g, device="cuda", dtype=torch.int32)
+    val = torch.randn(B, K, generator=g, device="cuda") * 4
+    lse = torch.logsumexp(val * 2, 1)
+    z = student(B, C, "f32", 7)
+    for shift in (None, 0.0, 12.0, -3.0):
+        check_distill(z, idx, val, "f32", None if shift is None else lse + shift, T=0.5,
+                      reduction=NONE)
+
+
 @pytest.mark.parametrize("B,C", KERNELS)
 def test_cold_and_hot(B, C):
     """Temperatures at which the softmax is one class, and uniform."""
