@@ -984,7 +984,7 @@ cudaError_t resident(const void *f, int threads, int smem, int *n) {
 // Shared memory of an SM, and what a CTA of the ring needs beside the ring
 // and its lists (the system's 1 KB and the kernel's static part, under 2 KB).
 constexpr int kSmemPerSm = 228 * 1024;
-constexpr int kSmemReserve = 3072;
+constexpr int kSmemReserve = 3 * 1024;
 
 cudaError_t plan_distill(long long B, long long C, int K, int dtype, bool grad, int sms,
                          DistillPlan *pl) {
